@@ -1,0 +1,58 @@
+// linattn_common.cuh -- what the kernels of linear attention share: one "pass" of the operator, its
+// decay factors and its addressing.
+//
+// A pass computes, for every sequence and head and in scan order (forward or reverse),
+//   S_t = gamma S_(t-1) + s_in k_t v_t^T,   y_t = q_t . S_t       (shift = 0), or
+//   A_t = R_t + s_in k_t v_t^T,  y_t = q_t . A_t,  R_(t+1) = gamma A_t   (shift = 1)
+// with y scaled by s_out.  shift = 1 is the adjoint's form: the decay stands behind the token, not before it.
+// The forward operator is the pass (q, k, v); its gradients are three more passes of the same kind:
+//   dq = (dy, v, k)  forward, state transposed     dv = (k, q, dy) against the scan order, shift 1
+//   dk = (v, dy, q)  against the scan order, shift 1, state transposed
+#pragma once
+
+#include "../common.cuh"
+
+namespace r2l {
+
+struct LaPass {
+    const void *q, *k, *v;
+    void* y;
+    long long q_tok, k_tok, v_tok, y_tok;  // elements from token to token
+    int nseq, seq_len, heads;              // a sequence: a batch row, or a block of one
+    int q_div, k_div, v_div;               // head h reads q head h / q_div, ...
+    int dk, dv;
+    int reverse, shift;
+    int y_f32;                             // y is fp32 whatever the inputs' type
+    const float* log_decay;
+    const int* lens;                       // [nseq] or NULL
+    const float* h0;                       // [nseq][heads] states or NULL
+    float* h_last;
+    int h_t;                               // states are stored [dv][dk] instead of [dk][dv]
+    float s_in, s_out;
+};
+
+// A decay of -inf would turn e^(0 * g) into NaN; e^-10000 is zero and its zeroth power one.
+__device__ __forceinline__ float la_clamp_decay(float g) { return g < -1e4f ? -1e4f : g; }
+
+// e^(g n) in fp32 from the exact product g n (the product's rounding error is put back to first order).
+__device__ __forceinline__ float la_decay_pow(float g, float n) {
+    const float x = g * n;
+    const float e = expf(x);
+    return fmaf(e, fmaf(g, n, -x), e);
+}
+
+// e^(g n) as the sum of two fp32 numbers: a state that is multiplied by it thousands of times keeps fp32
+// precision (one fp32 factor is 2^-25 off, the same way each time: 2.4e-4 after 8192 tokens).
+__device__ __forceinline__ void la_decay_pair(float g, float n, float& hi, float& lo) {
+    const double e = exp((double)g * (double)n);
+    hi = (float)e;
+    lo = (float)(e - (double)hi);
+}
+
+__device__ __forceinline__ int la_len(const LaPass& p, int seq) {
+    if (!p.lens) return p.seq_len;
+    const int n = p.lens[seq];
+    return n < 0 ? 0 : (n > p.seq_len ? p.seq_len : n);
+}
+
+}  // namespace r2l
