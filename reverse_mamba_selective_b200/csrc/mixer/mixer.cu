@@ -9,6 +9,7 @@
 #include "../common.cuh"
 #include "linattn_common.cuh"
 #include "linattn_rec.cuh"
+#include "linattn_tc.cuh"
 #include "qk_norm_rope.cuh"
 
 namespace r2l {
@@ -92,11 +93,23 @@ LaPass forward_pass(const r2l_linattn_args* a, const float* h0, float* h_last, v
     return p;
 }
 
-cudaError_t run_pass(const LaPass& p, r2l_dtype dtype, cudaStream_t stream) {
+// bf16 runs of more than a few tokens go to the tensor cores, token by token otherwise.
+bool on_tensor_cores(r2l_dtype dtype, int seq_len) { return dtype == R2L_BF16 && seq_len > 8; }
+
+// Workspace of one pass (the states between a divided sequence's segments).
+size_t pass_bytes(const r2l_linattn_args* a) {
+    const int nblk = a->reverse ? a->seqlen / a->block_len : 1, len = a->seqlen / nblk;
+    if (!on_tensor_cores(a->dtype, len)) return 0;
+    return align256(la_segment_bytes(a->batch * nblk, a->n_heads, len, a->d_k, a->d_v, sm_count()));
+}
+
+bool run_pass(const LaPass& p, r2l_dtype dtype, void* seg, cudaStream_t stream) {
     const int nsm = sm_count();
-    if (dtype == R2L_F32) return linattn_rec_launch<float, float>(p, nsm, stream);
-    if (p.y_f32) return linattn_rec_launch<__nv_bfloat16, float>(p, nsm, stream);
-    return linattn_rec_launch<__nv_bfloat16, __nv_bfloat16>(p, nsm, stream);
+    if (on_tensor_cores(dtype, p.seq_len)) return linattn_tc_launch(p, static_cast<float*>(seg), nsm, stream);
+    const cudaError_t e = dtype == R2L_F32 ? linattn_rec_launch<float, float>(p, nsm, stream)
+                          : p.y_f32        ? linattn_rec_launch<__nv_bfloat16, float>(p, nsm, stream)
+                                           : linattn_rec_launch<__nv_bfloat16, __nv_bfloat16>(p, nsm, stream);
+    return cuda_ok(e, "linear attention kernel launch");
 }
 
 r2l_status copy_state(const float* h0, float* h_last, size_t n, cudaStream_t stream) {
@@ -129,7 +142,7 @@ extern "C" {
 
 size_t r2l_linattn_workspace_size(const r2l_linattn_args* a) {
     if (check_linattn(a) != R2L_OK || la_empty(a) || a->seqlen == 0) return 0;
-    return 0;
+    return pass_bytes(a);
 }
 
 r2l_status r2l_linattn(const r2l_linattn_args* a, const float* h0, float* h_last, void* y, void* workspace,
@@ -142,8 +155,7 @@ r2l_status r2l_linattn(const r2l_linattn_args* a, const float* h0, float* h_last
     if (a->seqlen == 0) return copy_state(h0, h_last, (size_t)a->batch * a->n_heads * a->d_k * a->d_v, stream);
     if (!y || !aligned16(y)) return R2L_ERR_INVALID_ARG;
     if (bad_workspace(workspace, workspace_bytes, r2l_linattn_workspace_size(a))) return R2L_ERR_INVALID_ARG;
-    return cuda_ok(run_pass(forward_pass(a, h0, h_last, y), a->dtype, stream), "linear attention kernel launch") ? R2L_OK
-                                                                                                             : R2L_ERR_CUDA;
+    return run_pass(forward_pass(a, h0, h_last, y), a->dtype, workspace, stream) ? R2L_OK : R2L_ERR_CUDA;
 }
 
 r2l_status r2l_linattn_step(const r2l_linattn_args* a, const float* h, float* h_out, void* y, cudaStream_t stream) {
@@ -160,7 +172,7 @@ r2l_status r2l_linattn_step(const r2l_linattn_args* a, const float* h, float* h_
 
 size_t r2l_linattn_bwd_workspace_size(const r2l_linattn_args* a) {
     if (check_linattn(a) != R2L_OK || la_empty(a) || a->seqlen == 0) return 0;
-    return bwd_part_bytes(a);
+    return bwd_part_bytes(a) + pass_bytes(a);
 }
 
 r2l_status r2l_linattn_bwd(const r2l_linattn_args* a, const void* dy, const float* h0, const float* dh_last, void* dq,
@@ -177,13 +189,14 @@ r2l_status r2l_linattn_bwd(const r2l_linattn_args* a, const void* dy, const floa
 
     const LaPass f = forward_pass(a, h0, nullptr, nullptr);
     const long long rows = (long long)a->batch * a->seqlen, dy_tok = (long long)a->n_heads * a->d_v;
+    void* seg = static_cast<unsigned char*>(workspace) + bwd_part_bytes(a);
     // one pass into the gradient itself, or (shared heads) into the workspace and summed from there
     auto gradient = [&](LaPass p, void* out, int groups) -> bool {
         const int div = a->n_heads / groups;
         p.y_tok = (long long)a->n_heads * p.dv;
         p.y = div > 1 ? workspace : out;
         p.y_f32 = div > 1;
-        if (!cuda_ok(run_pass(p, a->dtype, stream), "linear attention gradient launch")) return false;
+        if (!run_pass(p, a->dtype, seg, stream)) return false;
         if (div == 1) return true;
         const size_t n = (size_t)rows * groups * p.dv;
         const unsigned blocks = (unsigned)std::min<size_t>((n + 255) / 256, 148 * 16);
