@@ -43,10 +43,15 @@ __device__ __forceinline__ float la_decay_pow(float g, float n) {
 
 // e^(g n) as the sum of two fp32 numbers: a state that is multiplied by it thousands of times keeps fp32
 // precision (one fp32 factor is 2^-25 off, the same way each time: 2.4e-4 after 8192 tokens).
-__device__ __forceinline__ void la_decay_pair(float g, float n, float& hi, float& lo) {
+__device__ __noinline__ float2 la_decay_pair_of(float g, float n) {
     const double e = exp((double)g * (double)n);
-    hi = (float)e;
-    lo = (float)(e - (double)hi);
+    const float hi = (float)e;
+    return make_float2(hi, (float)(e - (double)hi));
+}
+__device__ __forceinline__ void la_decay_pair(float g, float n, float& hi, float& lo) {
+    const float2 e = la_decay_pair_of(g, n);
+    hi = e.x;
+    lo = e.y;
 }
 
 __device__ __forceinline__ int la_len(const LaPass& p, int seq) {

@@ -17,16 +17,16 @@
 //
 // One CTA per SM walks over its (sequence, head) items; 16 warps with fixed roles:
 //   0-7   state: K~ from the K tile; S's operand copy; the update of S
-//   8-11  epilogue: y from the two accumulators, straight to global memory (a warp writes 32 neighbouring
-//         channels of a token)
-//   12-13 scores: QK -> P
+//   8-11  epilogue: y from the two accumulators, 32 channels a warp, transposed by stmatrix into the chunk's dead
+//         Q (and K) tile and stored from there by TMA
+//   12-13 scores: QK -> P, 32 tokens a warp, in blocks of 32 x 32: one on the diagonal, one full, one zero
 //   14    TMA producer (ring of chunk tiles), 15 MMA issuer
 // Bound by memory for heads of 64 to 128: a chunk moves 64 KB (d = 128), 1.5 us of an SM's share of the
 // bandwidth, against 0.7 us of tensor time.
 //
-// Masked places never reach an output: scores are selected, not multiplied, rows past a sequence's length are
-// zeroed where they would meet a zero weight, and a chunk whose P V product is not finite is summed again from
-// shared memory over its unmasked pairs (a zero weight times a later token's infinity is NaN).
+// Masked places never reach an output: rows of V past a sequence's length are zeroed, keys past it are not read into
+// K~, and where an output comes out not finite (a masked weight is a zero factor, and zero times an infinity is
+// NaN) the chunk's scores and values, still in shared memory, are summed again over the unmasked pairs alone.
 //
 // Every wait is bounded; one that runs out sets the device status word and the CTA stops.
 #pragma once
@@ -43,6 +43,7 @@ constexpr int kLaBlock = 8192;    // 64 tokens x 64 channels of bf16
 
 struct TcLaunch {
     CUtensorMap tq, tk, tv;       // [seq][token][head][channel], boxes of box_rows tokens x 64 channels
+    CUtensorMap ty;               // y the same way, boxes of box_rows x 32 (bf16 outputs)
     LaPass p;
     float* seg;                   // [item][nseg] states after the segments but the last, then h0's copy; or NULL
     int nseg, seg_chunks;         // segments of a sequence, chunks in each
@@ -57,7 +58,7 @@ struct LaCfg {
     static constexpr int StageBytes = QBytes + KBytes + VBytes;
     static constexpr int KtBytes = 3 * KBytes;
     static constexpr int PBytes = Y ? 2 * kLaBlock : 0;  // two parts
-    static constexpr int Free = 232448 - 1024 /*align*/ - 8192 /*static*/ - 512 /*barriers*/ - KtBytes - PBytes;
+    static constexpr int Free = 232448 - 1024 /*align*/ - 2048 /*static*/ - 512 /*barriers*/ - KtBytes - PBytes;
     static constexpr int Stages = Free / StageBytes > 6 ? 6 : Free / StageBytes;
     static constexpr int SmemBytes = 1024 + Stages * StageBytes + KtBytes + PBytes + 512;
     // tensor memory columns
@@ -95,6 +96,31 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16])
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
         : "memory");
 }
+// 64 fp32 columns of 16 lanes as 8 x 8 fragments: r[4 k + 2 a + b] is lane t / 4 + 8 a, column 8 k + 2 (t % 4) + b for
+// thread t of the warp; issued without waiting (tc_wait_ld32 completes it).
+__device__ __forceinline__ void tc_ld_frag_issue(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// Two 8 x 8 matrices of 16-bit values, stored transposed; lane l gives the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void st_matrix2_trans(uint32_t saddr, uint32_t a, uint32_t b) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(saddr), "r"(a), "r"(b) : "memory");
+}
+
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(src))
+                 : "memory");
+}
+
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
@@ -105,8 +131,19 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
+// Waits for the phase with the given parity, at most kWaitLimitNs; the same answer for the whole warp.  The clock is
+// read every 32 polls only: the busy warps need the issue slots.
+__device__ __noinline__ bool la_wait_long(uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    bool ok = false;
+    do {
+#pragma unroll 1
+        for (int i = 0; i < 32 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+    } while (!ok && globaltimer_ns() - t0 <= kWaitLimitNs);
+    return __all_sync(0xffffffffu, ok);
+}
 __device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || la_wait_long(bar, parity);
 }
 
 // One (sequence, head, segment): chunks a .. b - 1 in scan order of the nch chunks of its sequence.
@@ -160,8 +197,40 @@ __device__ __forceinline__ void la_chunk(const LaPass& p, const LaItem& it, int 
     n = min(kLaTok, it.len - row0);
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 la_fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+          "l"(*reinterpret_cast<unsigned long long*>(&c)));
+    return d;
+}
+__device__ __forceinline__ float2 la_mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<unsigned long long*>(&d))
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return d;
+}
+
 __device__ __forceinline__ float la_bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float la_bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// x rounded to two bf16; x becomes what the rounding left (exact).
+__device__ __forceinline__ uint32_t la_split(float2& x) {
+    const uint32_t w = pack_bf16x2(x.x, x.y);
+    x = la_fma2(make_float2(la_bf16_lo(w), la_bf16_hi(w)), make_float2(-1.f, -1.f), x);
+    return w;
+}
+
+// max(|m|, |w|) of the bf16 halves, NaN if either is.
+__device__ __forceinline__ uint32_t la_absmax_bf16x2(uint32_t m, uint32_t w) {
+    uint32_t d;
+    asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %2;\n\tmax.NaN.bf16x2 %0, %1, a;\n\t}\n" : "=r"(d) : "r"(m), "r"(w));
+    return d;
+}
+__device__ __forceinline__ bool la_not_finite(uint32_t m) { return (m & 0x7F80u) == 0x7F80u || (m & 0x7F800000u) == 0x7F800000u; }
 
 // Rows n .. of a chunk's V tile become zero (they stand behind the sequence's length: whatever they hold must
 // not meet a zero weight).
@@ -173,6 +242,22 @@ __device__ __forceinline__ void la_zero_rows(unsigned char* v, int vb, int n, in
     }
 }
 
+// sum over j0 <= j < j1 of P[i][j] V[j][ch], from the swizzled tiles (P in two parts).  Not inlined: it is for chunks
+// that hold infinities or NaN only, and the code around it has to stay in the instruction cache.
+__device__ __noinline__ float la_dot(const unsigned char* pt, const unsigned char* vt, int i, int ch, int j0, int j1) {
+    float acc = 0.f;
+#pragma unroll 1
+    for (int j = j0; j < j1; ++j) {
+        const unsigned char* pa = pt + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2;
+        const float pw = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(pa)) +
+                         __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(pa + kLaBlock));
+        const float vv = __bfloat162float(
+            *reinterpret_cast<const __nv_bfloat16*>(vt + j * 128 + (((ch >> 3) ^ (j & 7)) << 4) + (ch & 7) * 2));
+        acc = fmaf(pw, vv, acc);
+    }
+    return acc;
+}
+
 template <int DK, int DV, bool Y>
 __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_constant__ TcLaunch L) {
     using Cfg = LaCfg<DK, DV, Y>;
@@ -180,8 +265,8 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    // decay tables of the item that a warp is at; each warp has its own, as the warps are at different items
-    __shared__ float tab[14][2 * kLaTok];
+    // decay tables of the epilogue's and the scores' warps, one each: the warps are at different items
+    __shared__ __align__(16) float tab[6][kLaTok];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* kt = smem + NST * Cfg::StageBytes;
@@ -192,9 +277,8 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
     uint64_t* qk_empty = qk_full + 2;  // [2]
     uint64_t* p_full = qk_empty + 2;
     uint64_t* p_empty = p_full + 1;
-    uint64_t* kt_go = p_empty + 1;
-    uint64_t* kt_full = kt_go + 1;
-    uint64_t* kv_full = kt_full + 1;
+    uint64_t* kt_full = p_empty + 1;   // [NST]: one phase per chunk, whether or not its keys are needed
+    uint64_t* kv_full = kt_full + NST;
     uint64_t* s_full = kv_full + 1;
     uint64_t* qs_done = s_full + 1;
     uint64_t* o_full = qs_done + 1;
@@ -202,11 +286,12 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
 
     const LaPass& p = L.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    float* wtab = tab[min(warp, 13)];
+    float* wtab = tab[warp >= 8 && warp < 14 ? warp - 8 : 0];
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], Y ? 5 : 1);  // the last MMA, and the four epilogue warps
+            mbar_init(&kt_full[i], 256);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&qk_full[i], 1);
@@ -214,8 +299,6 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         }
         mbar_init(p_full, 64);
         mbar_init(p_empty, 4);
-        mbar_init(kt_go, 1);
-        mbar_init(kt_full, 256);
         mbar_init(kv_full, 1);
         mbar_init(s_full, 256);
         mbar_init(qs_done, 1);
@@ -270,7 +353,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         constexpr uint32_t kDesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);  // fp32 += bf16 bf16, M 128
         constexpr uint32_t kMnA = 1u << 15, kMnB = 1u << 16;
         const uint32_t n_tok = (uint32_t)(L.n16 >> 3) << 17, n_dk = (uint32_t)(DK >> 3) << 17;
-        const int kd_steps = (p.dk + 15) >> 4, tok_steps = L.n16 >> 4;
+        const int tok_steps = L.n16 >> 4;
         const uint64_t dq = sw128_kmajor_desc(smem_addr(smem)), dk = sw128_kmajor_desc(smem_addr(smem + Cfg::QBytes));
         const uint64_t dv = la_mn_desc(smem_addr(smem + Cfg::QBytes + Cfg::KBytes));
         const uint64_t dkt = la_mn_desc(smem_addr(kt)), dp = sw128_kmajor_desc(smem_addr(pbuf));
@@ -286,7 +369,8 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
             tc_fence_after();
             if (elect_one()) {
                 const uint64_t so = stage_off(pos);
-                for (int kk = 0; kk < kd_steps; ++kk) {
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk) {
                     const uint64_t o = so + (uint64_t)(((kk >> 2) * kLaBlock + (kk & 3) * 32) >> 4);
                     tc_mma(tmem + Cfg::QK + (pos & 1) * 64, dq + o, dk + o, kDesc | n_tok, kk > 0);
                 }
@@ -295,7 +379,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
             __syncwarp();
             return true;
         };
-        uint32_t pos = 0, nkv = 0, nqs = 0, nqk = 0;
+        uint32_t pos = 0, nqs = 0, nqk = 0;
         for (int work = blockIdx.x; work < L.nwork && ok; work += gridDim.x) {
             const LaItem it = la_item<Y>(L, work);
             for (int c = it.a; c < it.b && ok; ++c, ++pos) {
@@ -303,25 +387,26 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                 const int st = pos % NST;
                 const uint64_t so = stage_off(pos);
                 if (!(ok = la_wait(&full[st], (pos / NST) & 1u))) break;
-                if (need && lane == 0) mbar_arrive(kt_go);
                 if (Y && nqk == pos) {
                     if (!(ok = scores(pos))) break;
                     nqk = pos + 1;
                 }
+                if (!(ok = la_wait(&kt_full[st], (pos / NST) & 1u))) break;
                 if (need) {
-                    if (!(ok = la_wait(kt_full, nkv & 1u))) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        for (int part = 0; part < L.nsplit; ++part)
-                            for (int kk = 0; kk < tok_steps; ++kk)
-                                tc_mma(tmem + Cfg::KV, dv + so + (uint64_t)(kk * 2048 >> 4),
-                                       dkt + (uint64_t)((part * Cfg::KBytes + kk * 2048) >> 4), kDesc | kMnA | kMnB | n_dk,
-                                       part > 0 || kk > 0);
+#pragma unroll
+                        for (int part = 0; part < 3; ++part)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                if (part < L.nsplit && kk < tok_steps)
+                                    tc_mma(tmem + Cfg::KV, dv + so + (uint64_t)(kk * 2048 >> 4),
+                                           dkt + (uint64_t)((part * Cfg::KBytes + kk * 2048) >> 4), kDesc | kMnA | kMnB | n_dk,
+                                           part > 0 || kk > 0);
                         tc_commit(kv_full);
                         if (!Y) tc_commit(&empty[st]);
                     }
                     __syncwarp();
-                    ++nkv;
                 }
                 if (Y) {
                     // the next chunk's scores early, if its tiles are there
@@ -335,8 +420,10 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                         if (!(ok = la_wait(s_full, nqs & 1u))) break;
                         tc_fence_after();
                         if (elect_one()) {
+#pragma unroll
                             for (int part = 0; part < 2; ++part)
-                                for (int kk = 0; kk < kd_steps; ++kk)
+#pragma unroll
+                                for (int kk = 0; kk < DK / 16; ++kk)
                                     tc_mma_ts(tmem + Cfg::OI, tmem + Cfg::SB + part * (DK / 2) + kk * 8,
                                               dq + so + (uint64_t)(((kk >> 2) * kLaBlock + (kk & 3) * 32) >> 4), kDesc | n_tok,
                                               part > 0 || kk > 0);
@@ -348,10 +435,13 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     if (!(ok = la_wait(p_full, pos & 1u))) break;
                     tc_fence_after();
                     if (elect_one()) {
+#pragma unroll
                         for (int part = 0; part < 2; ++part)
-                            for (int kk = 0; kk < tok_steps; ++kk)
-                                tc_mma(tmem + Cfg::OA, dv + so + (uint64_t)(kk * 2048 >> 4),
-                                       dp + (uint64_t)((part * kLaBlock + kk * 32) >> 4), kDesc | kMnA | n_tok, part > 0 || kk > 0);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                if (kk < tok_steps)
+                                    tc_mma(tmem + Cfg::OA, dv + so + (uint64_t)(kk * 2048 >> 4),
+                                           dp + (uint64_t)((part * kLaBlock + kk * 32) >> 4), kDesc | kMnA | n_tok, part > 0 || kk > 0);
                         tc_commit(o_full);
                         tc_commit(&empty[st]);
                     }
@@ -368,17 +458,12 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         const bool rows_used = quarter * 32 < DV;   // warp-uniform
         const bool live = row < p.dv;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        float S[H];
+        float2 S[H / 2];
         uint32_t pos = 0, nkv = 0, nqs = 0;
         for (int work = blockIdx.x; work < L.nwork && ok; work += gridDim.x) {
             const LaItem it = la_item<Y>(L, work);
-            const bool carries = it.in || it.out || it.b - it.a > 1;
-            if (!carries) {
-                pos += (uint32_t)(it.b - it.a);
-                continue;
-            }
 #pragma unroll
-            for (int i = 0; i < H; ++i) S[i] = 0.f;
+            for (int i = 0; i < H / 2; ++i) S[i] = make_float2(0.f, 0.f);
             if (it.in && live) {
                 if (it.in_t) {
                     const float* a = it.in + (size_t)row * p.dk + k0;
@@ -386,58 +471,67 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     for (int i = 0; i < H; i += 4)
                         if (k0 + i < p.dk) {
                             const float4 x = *reinterpret_cast<const float4*>(a + i);
-                            S[i] = x.x, S[i + 1] = x.y, S[i + 2] = x.z, S[i + 3] = x.w;
+                            S[i / 2] = make_float2(x.x, x.y);
+                            S[i / 2 + 1] = make_float2(x.z, x.w);
                         }
                 } else {
                     const float* a = it.in + (size_t)k0 * p.dv + row;
 #pragma unroll
-                    for (int i = 0; i < H; ++i)
-                        if (k0 + i < p.dk) S[i] = a[(size_t)i * p.dv];
+                    for (int i = 0; i < H; i += 2)  // dk is a multiple of 8
+                        if (k0 + i < p.dk) S[i / 2] = make_float2(a[(size_t)i * p.dv], a[(size_t)(i + 1) * p.dv]);
                 }
             }
-            __syncwarp();
-            for (int i = lane; i <= kLaTok; i += 32) wtab[i] = p.s_in * la_decay_pow(it.g, (float)i);  // s_in gamma^i
-            __syncwarp();
-            float ghi, glo;
-            la_decay_pair(it.g, (float)kLaTok, ghi, glo);
+            // of a full chunk: its decay, and the weights of the two tokens whose keys this thread scales
+            float ghi, glo, kw[2], dhi, dlo;
+            int kw_n = -1;
+            if (it.b - it.a > 1 || it.out) la_decay_pair(it.g, (float)kLaTok, ghi, glo);
             for (int c = it.a; c < it.b; ++c, ++pos) {
                 const bool has = it.in || c > it.a, need = c < it.b - 1 || it.out;
                 int row0, n;
                 la_chunk(p, it, c, row0, n);
+                const int st = pos % NST;
+                if (!(ok = la_wait(&full[st], (pos / NST) & 1u))) break;
                 if (need) {
-                    const int st = pos % NST;
-                    if (!(ok = la_wait(kt_go, nkv & 1u) && la_wait(&full[st], (pos / NST) & 1u))) break;
                     unsigned char* s = smem + st * Cfg::StageBytes;
-                    // K~: the swizzle only permutes 16-byte pieces within a token's row
+                    if (n != kw_n) {
+                        kw_n = n;
+                        dhi = ghi, dlo = glo;
+                        if (n != kLaTok) la_decay_pair(it.g, (float)n, dhi, dlo);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int j = (tid >> 3) + 32 * e;
+                            kw[e] = j < n ? p.s_in * la_decay_pow(it.g, (float)((p.reverse ? j : n - 1 - j) + p.shift)) : 0.f;
+                        }
+                    }
+                    // K~: the swizzle only permutes 16-byte pieces within a token's row.  Piece tid + 256 m belongs to token
+                    // tid / 8 + 32 (m % 2); all pieces are fetched before the first is written
+                    uint4 x[Cfg::KB * 2];
 #pragma unroll
                     for (int m = 0; m < Cfg::KB * 2; ++m) {
-                        const int u = tid + m * 256, j = (u >> 3) & 63;
-                        if (j >= L.n16) continue;
-                        uint32_t hi[4] = {0, 0, 0, 0}, mid[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-                        if (j < n) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(s + Cfg::QBytes + u * 16);
-                            const float w = wtab[(p.reverse ? j : n - 1 - j) + p.shift];
-                            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                        x[m] = make_uint4(0, 0, 0, 0);
+                        if ((tid >> 3) + 32 * (m & 1) < n) x[m] = *reinterpret_cast<const uint4*>(s + Cfg::QBytes + (tid + m * 256) * 16);
+                    }
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float a = la_bf16_lo(xs[e]) * w, b = la_bf16_hi(xs[e]) * w;
-                                hi[e] = pack_bf16x2(a, b);
-                                a -= la_bf16_lo(hi[e]);
-                                b -= la_bf16_hi(hi[e]);
-                                mid[e] = pack_bf16x2(a, b);
-                                if (L.nsplit > 2) lo[e] = pack_bf16x2(a - la_bf16_lo(mid[e]), b - la_bf16_hi(mid[e]));
-                            }
+                    for (int m = 0; m < Cfg::KB * 2; ++m) {
+                        const float2 w = make_float2(kw[m & 1], kw[m & 1]);
+                        const uint32_t xs[4] = {x[m].x, x[m].y, x[m].z, x[m].w};
+                        float2 a[4];
+                        uint32_t t[4];
+                        unsigned char* o = kt + (tid + m * 256) * 16;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a[e] = la_mul2(make_float2(la_bf16_lo(xs[e]), la_bf16_hi(xs[e])), w);
+#pragma unroll
+                        for (int part = 0; part < 3; ++part) {
+                            if (part == 2 && L.nsplit < 3) break;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) t[e] = part < 2 ? la_split(a[e]) : pack_bf16x2(a[e].x, a[e].y);
+                            *reinterpret_cast<uint4*>(o + part * Cfg::KBytes) = make_uint4(t[0], t[1], t[2], t[3]);
                         }
-                        unsigned char* o = kt + u * 16;
-                        *reinterpret_cast<uint4*>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(o + Cfg::KBytes) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                        if (L.nsplit > 2)
-                            *reinterpret_cast<uint4*>(o + 2 * Cfg::KBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                     if (n < kLaTok && row0 + n < p.seq_len) la_zero_rows(s + Cfg::QBytes + Cfg::KBytes, Cfg::VB, n, tid, 256);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive(kt_full);
                 }
+                mbar_arrive(&kt_full[st]);
                 if (Y && has) {
                     // the operand copy of S, once the previous chunk's product has read the last one
                     if (!(ok = la_wait(qs_done, (nqs & 1u) ^ 1u))) break;
@@ -448,11 +542,14 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                             uint32_t w[16];
                             const uint32_t to = tmem + lane_off + Cfg::SB + half * (H / 2) + q * 16;
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(S[q * 32 + 2 * e], S[q * 32 + 2 * e + 1]);
+                            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(S[q * 16 + e].x, S[q * 16 + e].y);
                             tc_st16(to, w);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                w[e] = pack_bf16x2(S[q * 32 + 2 * e] - la_bf16_lo(w[e]), S[q * 32 + 2 * e + 1] - la_bf16_hi(w[e]));
+                            for (int e = 0; e < 16; ++e) {
+                                float2 x = S[q * 16 + e];
+                                la_split(x);
+                                w[e] = pack_bf16x2(x.x, x.y);
+                            }
                             tc_st16(to + DK / 2, w);
                         }
                         tc_wait_st();
@@ -462,8 +559,6 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     ++nqs;
                 }
                 if (need) {
-                    float dhi = ghi, dlo = glo;
-                    if (n != kLaTok) la_decay_pair(it.g, (float)n, dhi, dlo);
                     if (!(ok = la_wait(kv_full, nkv & 1u))) break;
                     ++nkv;
                     tc_fence_after();
@@ -474,9 +569,10 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                             tc_ld32_issue(tmem + lane_off + Cfg::KV + k0 + q * 32, r);
                             tc_wait_ld32(r);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float x = S[q * 32 + e];
-                                S[q * 32 + e] = fmaf(x, dhi, fmaf(x, dlo, __uint_as_float(r[e])));
+                            for (int e = 0; e < 16; ++e) {
+                                const float2 x = S[q * 16 + e];
+                                const float2 kv = make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+                                S[q * 16 + e] = la_fma2(x, make_float2(dhi, dhi), la_fma2(x, make_float2(dlo, dlo), kv));
                             }
                         }
                     }
@@ -488,169 +584,207 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     float* a = it.out + (size_t)row * p.dk + k0;
 #pragma unroll
                     for (int i = 0; i < H; i += 4)
-                        if (k0 + i < p.dk) *reinterpret_cast<float4*>(a + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+                        if (k0 + i < p.dk) *reinterpret_cast<float4*>(a + i) = make_float4(S[i / 2].x, S[i / 2].y, S[i / 2 + 1].x, S[i / 2 + 1].y);
                 } else {
                     float* a = it.out + (size_t)k0 * p.dv + row;
 #pragma unroll
                     for (int i = 0; i < H; ++i)
-                        if (k0 + i < p.dk) a[(size_t)i * p.dv] = S[i];
+                        if (k0 + i < p.dk) a[(size_t)i * p.dv] = i & 1 ? S[i / 2].y : S[i / 2].x;
                 }
             }
         }
     } else if (Y && warp < 12) {
         // ------------------------------------------------------------------ epilogue
-        const int quarter = warp & 3, row = quarter * 32 + lane;
-        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const bool rows_used = quarter * 32 < DV, live = row < p.dv;
+        const int quarter = warp & 3, c0 = quarter * 32;  // this warp's channels c0 .. c0 + 31
+        const uint32_t lane_off = (uint32_t)c0 << 16;
+        const bool used = c0 < p.dv;                      // warp-uniform
+        const int fr = lane >> 2, fc = (lane & 3) * 2;    // this thread's row and column of an 8 x 8 fragment
         uint32_t pos = 0;
         for (int work = blockIdx.x; work < L.nwork && ok; work += gridDim.x) {
             const LaItem it = la_item<Y>(L, work);
-            __syncwarp();
-            for (int i = lane; i <= kLaTok; i += 32) wtab[i] = p.s_out * la_decay_pow(it.g, (float)i);  // s_out gamma^i
-            __syncwarp();
-            const size_t base = (size_t)it.seq * p.seq_len * p.y_tok + (size_t)it.h * p.dv + row;
-            float* yf = static_cast<float*>(p.y) + base;
-            __nv_bfloat16* yb = static_cast<__nv_bfloat16*>(p.y) + base;
+            float2 fac[8];  // s_out gamma^(position + 1 - shift) of tokens 8 k + fc, 8 k + fc + 1
+            int fac_n = -1;
             for (int c = it.a; c < it.b; ++c, ++pos) {
                 const bool has = it.in || c > it.a;
                 const int st = pos % NST;
                 int row0, n;
                 la_chunk(p, it, c, row0, n);
+                if (has && n != fac_n) {
+                    fac_n = n;
+                    __syncwarp();
+#pragma unroll
+                    for (int i = lane; i < kLaTok; i += 32)
+                        wtab[i] = i < n ? p.s_out * la_decay_pow(it.g, (float)((p.reverse ? n - 1 - i : i) + 1 - p.shift)) : 0.f;
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) fac[k] = *reinterpret_cast<const float2*>(wtab + 8 * k + fc);
+                }
                 if (!(ok = la_wait(o_full, pos & 1u))) break;
                 tc_fence_after();
-                float o[kLaTok];
-                bool finite = true;
-                if (rows_used) {
-                    float any = 0.f;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t r[32];
-                        tc_ld32_issue(tmem + lane_off + Cfg::OA + q * 32, r);
+                unsigned char* tile = smem + st * Cfg::StageBytes + quarter * (kLaBlock / 2);
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {  // channels c0 + 16 half ..
+                    uint32_t r[32], s2[32];
+                    if (used) {
+                        const uint32_t ta = tmem + lane_off + ((uint32_t)(half * 16) << 16);
+                        tc_ld_frag_issue(ta + Cfg::OA, r);
+                        if (has) tc_ld_frag_issue(ta + Cfg::OI, s2);
                         tc_wait_ld32(r);
+                        if (has) tc_wait_ld32(s2);
+                        auto add_inter = [&] {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            o[q * 32 + e] = __uint_as_float(r[e]);
-                            if (q * 32 + e < n) any = fmaf(o[q * 32 + e], 0.f, any);  // NaN once anything is not finite
-                        }
-                    }
-                    finite = __all_sync(0xffffffffu, any == 0.f);
-                    if (!finite) {
-                        // a masked token may have met a zero weight: the same sums over the unmasked pairs alone
-                        la_wait(p_full, pos & 1u);
-                        la_wait(&full[st], (pos / NST) & 1u);
-                        const unsigned char* v = smem + st * Cfg::StageBytes + Cfg::QBytes + Cfg::KBytes + (row >> 6) * kLaBlock;
-                        const int ch = row & 63;
-#pragma unroll
-                        for (int i = 0; i < kLaTok; ++i) {
-                            if (i >= n) continue;
-                            const int j0 = p.reverse ? i : 0, j1 = p.reverse ? n : i + 1;
-                            float acc = 0.f;
-                            for (int j = j0; j < j1; ++j) {
-                                const unsigned char* pa = pbuf + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2;
-                                const float pw = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(pa)) +
-                                                 __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(pa + kLaBlock));
-                                const float vv = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
-                                    v + j * 128 + (((ch >> 3) ^ (j & 7)) << 4) + (ch & 7) * 2));
-                                acc = fmaf(pw, vv, acc);
+                            for (int k = 0; k < 16; ++k) {
+                                const float2 y = la_fma2(fac[k >> 1], make_float2(__uint_as_float(s2[2 * k]), __uint_as_float(s2[2 * k + 1])),
+                                                         make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])));
+                                r[2 * k] = __float_as_uint(y.x);
+                                r[2 * k + 1] = __float_as_uint(y.y);
                             }
-                            o[i] = acc;
-                        }
-                    }
-                    if (has) {
+                        };
+                        if (has) add_inter();
+                        uint32_t big = 0;
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t r[32];
-                            tc_ld32_issue(tmem + lane_off + Cfg::OI + q * 32, r);
-                            tc_wait_ld32(r);
-                            // gamma^(position + 1 - shift)
-                            const float* f = p.reverse ? wtab + (n - p.shift) : wtab + (1 - p.shift);
+                        for (int k = 0; k < 16; ++k)
+                            if (8 * (k >> 1) < L.n16)
+                                big = la_absmax_bf16x2(big, pack_bf16x2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])));
+                        if (__any_sync(0xffffffffu, la_not_finite(big))) {
+                            // a masked token may have met a zero weight: the sums over the unmasked pairs alone
+                            la_wait(p_full, pos & 1u);
+                            la_wait(&full[st], (pos / NST) & 1u);
+                            const unsigned char* vt = smem + st * Cfg::StageBytes + Cfg::QBytes + Cfg::KBytes + (c0 >> 6) * kLaBlock;
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
-                                const int i = q * 32 + e;
-                                const float w = p.reverse ? (i < n ? f[-i] : 0.f) : f[i];
-                                o[i] = fmaf(w, __uint_as_float(r[e]), o[i]);
+                                const int i = 8 * (e >> 2) + fc + (e & 1), ch = (c0 & 63) + half * 16 + fr + 8 * ((e >> 1) & 1);
+                                const int j0 = p.reverse ? i : 0, j1 = i >= n ? 0 : p.reverse ? n : i + 1;
+                                r[e] = __float_as_uint(la_dot(pbuf, vt, i, ch, j0, j1));
+                            }
+                            if (has) add_inter();
+                        }
+                        if (n != kLaTok) {  // rows past the length are stored as zeros (past seq_len: not at all)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (8 * (e >> 2) + fc + (e & 1) >= n) r[e] = 0u;
+                        }
+                    }
+                    if (half == 1) {
+                        // both accumulators, P and V have been read
+                        tc_fence_before();
+                        mbar_arrive(o_empty);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_empty);
+                    }
+                    if (used) {
+                        if (p.y_f32) {
+                            float* y = static_cast<float*>(p.y) + ((size_t)it.seq * p.seq_len + row0) * p.y_tok + (size_t)it.h * p.dv;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const int i = 8 * (e >> 2) + fc + (e & 1), ch = c0 + half * 16 + fr + 8 * ((e >> 1) & 1);
+                                if (row0 + i < p.seq_len && ch < p.dv) y[(size_t)i * p.y_tok + ch] = __uint_as_float(r[e]);
+                            }
+                        } else {
+                            // [token][32 channels], 64-byte rows, 16-byte pieces swizzled by the row pair
+                            const uint32_t ts = smem_addr(tile);
+                            const int tr = lane & 7, m = half * 2 + ((lane >> 3) & 1);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const int i = 8 * k + tr;
+                                st_matrix2_trans(ts + i * 64 + ((m ^ ((i >> 1) & 3)) << 4),
+                                                 pack_bf16x2(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1])),
+                                                 pack_bf16x2(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3])));
                             }
                         }
                     }
                 }
-                tc_fence_before();
-                mbar_arrive(o_empty);
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(p_empty);
-                    mbar_arrive(&empty[st]);
-                }
-                if (live) {
-                    if (p.y_f32) {
-                        float* y = yf + (size_t)row0 * p.y_tok;
-#pragma unroll
-                        for (int i = 0; i < kLaTok; ++i)
-                            if (i < n) y[(size_t)i * p.y_tok] = o[i];
-                    } else {
-                        __nv_bfloat16* y = yb + (size_t)row0 * p.y_tok;
-#pragma unroll
-                        for (int i = 0; i < kLaTok; ++i)
-                            if (i < n) y[(size_t)i * p.y_tok] = __float2bfloat16_rn(o[i]);
+                if (used && !p.y_f32) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_4d(&L.ty, tile, c0, it.h, row0, it.seq);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[st]);
             }
-            if (it.a == 0 && live && ok) {  // the first segment's CTA also writes the zeros behind the row's tokens
-                for (int t = it.len; t < p.seq_len; ++t) {
+            if (it.a == 0 && ok) {  // chunks that lie wholly behind the row's tokens: zeros
+                const int ch = c0 + lane;
+                for (int t = it.nch * kLaTok; t < p.seq_len && ch < p.dv; ++t) {
+                    const size_t o = ((size_t)it.seq * p.seq_len + t) * p.y_tok + (size_t)it.h * p.dv + ch;
                     if (p.y_f32)
-                        yf[(size_t)t * p.y_tok] = 0.f;
+                        static_cast<float*>(p.y)[o] = 0.f;
                     else
-                        yb[(size_t)t * p.y_tok] = __float2bfloat16_rn(0.f);
+                        static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(0.f);
                 }
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else if (Y && warp < 14) {
         // ------------------------------------------------------------------ scores
-        const int i = tid - 384;  // the row (token) of this thread
-        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const int w = warp - 12, i = 32 * w + lane;  // the row (token) of this thread
+        const uint32_t lane_off = (uint32_t)(32 * w) << 16;
+        unsigned char* pb = pbuf + i * 128;
+        // of the two blocks off the diagonal one is all masked: it stays zero
+        const bool full_block = p.reverse ? w == 0 : w == 1;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+                *reinterpret_cast<uint4*>(pb + part * kLaBlock + q * 16) = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        const float s = p.s_in * p.s_out;
         uint32_t pos = 0;
         for (int work = blockIdx.x; work < L.nwork && ok; work += gridDim.x) {
             const LaItem it = la_item<Y>(L, work);
-            const float s = p.s_in * p.s_out;
-            __syncwarp();
-            for (int d = lane - 63; d <= 63; d += 32) {  // s_in s_out gamma^|d| at 63 + d, zero where masked
-                const float w = s * la_decay_pow(it.g, (float)abs(d));
-                wtab[63 + d] = (p.reverse ? d <= 0 : d >= 0) ? w : 0.f;
+            // weights of this row: on the diagonal block, and on the full one (its columns are farther)
+            float2 wd[16], wo[16];
+            if (it.b > it.a) {
+                __syncwarp();
+                wtab[lane] = s * la_decay_pow(it.g, (float)lane);
+                wtab[lane + 32] = s * la_decay_pow(it.g, (float)(lane + 32));
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    auto diag = [&](int c) { return (p.reverse ? c >= lane : c <= lane) ? wtab[abs(lane - c)] : 0.f; };
+                    wd[j / 2] = make_float2(diag(j), diag(j + 1));
+                    wo[j / 2] = p.reverse ? make_float2(wtab[32 + j - lane], wtab[33 + j - lane])
+                                          : make_float2(wtab[32 + lane - j], wtab[31 + lane - j]);
+                }
             }
-            __syncwarp();
             for (int c = it.a; c < it.b; ++c, ++pos) {
                 int row0, n;
                 la_chunk(p, it, c, row0, n);
                 if (!(ok = la_wait(&qk_full[pos & 1], (pos >> 1) & 1u))) break;
                 tc_fence_after();
-                uint32_t r0[32], r1[32];
-                tc_ld32_issue(tmem + lane_off + Cfg::QK + (pos & 1) * 64, r0);
-                tc_ld32_issue(tmem + lane_off + Cfg::QK + (pos & 1) * 64 + 32, r1);
-                tc_wait_ld32(r0);
-                tc_wait_ld32(r1);
+                const uint32_t ta = tmem + lane_off + Cfg::QK + (pos & 1) * 64;
+                uint32_t r[32];
+                // 32 scores of this row, weighted, in two bf16 parts, to columns c0 .. c0 + 31 of P
+                auto put = [&](int col0, const float2 (&wt)[16]) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t a[4], b[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float2 x = la_mul2(make_float2(__uint_as_float(r[q * 8 + 2 * e]), __uint_as_float(r[q * 8 + 2 * e + 1])),
+                                               wt[q * 4 + e]);
+                            a[e] = la_split(x);
+                            b[e] = pack_bf16x2(x.x, x.y);
+                        }
+                        unsigned char* o = pb + ((((col0 >> 3) + q) ^ (i & 7)) << 4);
+                        *reinterpret_cast<uint4*>(o) = make_uint4(a[0], a[1], a[2], a[3]);
+                        *reinterpret_cast<uint4*>(o + kLaBlock) = make_uint4(b[0], b[1], b[2], b[3]);
+                    }
+                };
+                tc_ld32_issue(ta + 32 * w, r);
+                tc_wait_ld32(r);
+                if (!(ok = la_wait(p_empty, (pos & 1u) ^ 1u))) break;
+                put(32 * w, wd);
+                if (full_block && L.n16 > 32) {
+                    tc_ld32_issue(ta + 32 * (1 - w), r);
+                    tc_wait_ld32(r);
+                    put(32 * (1 - w), wo);
+                }
                 tc_fence_before();
                 mbar_arrive(&qk_empty[pos & 1]);
-                if (!(ok = la_wait(p_empty, (pos & 1u) ^ 1u))) break;
-                unsigned char* pb = pbuf + i * 128;
-                const float* t = wtab + 63 + i;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    uint32_t w[4], u[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v[2];
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const int j = q * 8 + e * 2 + b;
-                            const float x = __uint_as_float(j < 32 ? r0[j & 31] : r1[j & 31]);
-                            const float d = t[-j];
-                            v[b] = (d != 0.f && j < n) ? x * d : 0.f;
-                        }
-                        w[e] = pack_bf16x2(v[0], v[1]);
-                        u[e] = pack_bf16x2(v[0] - la_bf16_lo(w[e]), v[1] - la_bf16_hi(w[e]));
-                    }
-                    *reinterpret_cast<uint4*>(pb + ((q ^ (i & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4*>(pb + kLaBlock + ((q ^ (i & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-                }
                 if (n < kLaTok && row0 + n < p.seq_len) {
                     const int st = pos % NST;
                     if (!(ok = la_wait(&full[st], (pos / NST) & 1u))) break;
@@ -709,8 +843,10 @@ __global__ void __launch_bounds__(256) linattn_segments_kernel(LaPass p, float* 
 
 // ------------------------------------------------------------------------------------ host
 
-// [seq][token][head][channel] with the given element strides, boxes of box_rows tokens x 64 channels of a head.
-inline bool la_encode(CUtensorMap* out, const void* base, int d, int heads, int seq_len, int nseq, long long tok, int box_rows) {
+// [seq][token][head][channel] with the given element strides, boxes of box_rows tokens x box_cols (64 or 32) channels
+// of a head.
+inline bool la_encode(CUtensorMap* out, const void* base, int d, int heads, int seq_len, int nseq, long long tok, int box_rows,
+                      int box_cols = 64) {
     auto enc = tensor_map_encoder();
     if (!enc) {
         snprintf(last_error_buffer(), 256, "cuTensorMapEncodeTiled: driver entry point unavailable");
@@ -718,10 +854,11 @@ inline bool la_encode(CUtensorMap* out, const void* base, int d, int heads, int 
     }
     cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)seq_len, (cuuint64_t)nseq};
     cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)tok * 2, (cuuint64_t)tok * 2 * (cuuint64_t)seq_len};
-    cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
+    cuuint32_t box[4] = {(cuuint32_t)box_cols, 1, (cuuint32_t)box_rows, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     const CUresult r = enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r == CUDA_SUCCESS) return true;
     snprintf(last_error_buffer(), 256, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
@@ -776,6 +913,7 @@ inline bool linattn_tc_launch(const LaPass& p, float* seg, int nsm, cudaStream_t
         !la_encode(&L.tk, p.k, p.dk, p.heads / p.k_div, p.seq_len, p.nseq, p.k_tok, L.box_rows) ||
         !la_encode(&L.tv, p.v, p.dv, p.heads / p.v_div, p.seq_len, p.nseq, p.v_tok, L.box_rows))
         return false;
+    if (!p.y_f32 && !la_encode(&L.ty, p.y, p.dv, p.heads, p.seq_len, p.nseq, p.y_tok, L.box_rows, 32)) return false;
     if (L.nseg > 1) {
         L.nwork = p.nseq * p.heads * (L.nseg - 1);
         if (!la_tc_pick<false>(L, nsm, stream)) return false;
