@@ -47,7 +47,7 @@ struct TcLaunch {
     LaPass p;
     float* seg;                   // [item][nseg] states after the segments but the last, then h0's copy; or NULL
     int nseg, seg_chunks;         // segments of a sequence, chunks in each
-    int nwork, box_rows, n16;     // n16: box_rows rounded up to 16
+    int nwork, box_rows;
     int nsplit;                   // parts of K~
 };
 
@@ -57,34 +57,44 @@ struct LaCfg {
     static constexpr int QBytes = Y ? KB * kLaBlock : 0, KBytes = KB * kLaBlock, VBytes = VB * kLaBlock;
     static constexpr int StageBytes = QBytes + KBytes + VBytes;
     static constexpr int KtBytes = 3 * KBytes;
-    static constexpr int PBytes = Y ? 2 * kLaBlock : 0;  // two parts
-    static constexpr int Free = 232448 - 1024 /*align*/ - 2048 /*static*/ - 512 /*barriers*/ - KtBytes - PBytes;
+    static constexpr int PPart = kLaBlock, PBytes = Y ? 2 * 2 * PPart : 0;  // two buffers of two parts
+    static constexpr int TabBytes = 6 * kLaTok * 4, BarBytes = 256;
+    static constexpr int Fixed = 1024 /*alignment*/ + KtBytes + PBytes + TabBytes + BarBytes;
+    static constexpr int Free = 232448 - 64 /*static*/ - Fixed;
     static constexpr int Stages = Free / StageBytes > 6 ? 6 : Free / StageBytes;
-    static constexpr int SmemBytes = 1024 + Stages * StageBytes + KtBytes + PBytes + 512;
+    static constexpr int SmemBytes = Fixed + Stages * StageBytes;
+    static_assert((3 * Stages + 13) * 8 <= BarBytes, "barriers");
     // tensor memory columns
     static constexpr int QK = 0, OI = 128, OA = 192, KV = 256, SB = 384, Cols = 512;  // SB: two parts of DK / 2
     static_assert(Stages >= 2, "ring depth");
 };
 
-// MN-major tile with 128-byte swizzle: 64 channels (128 bytes) per token row, 8 tokens 1024 bytes apart (stride
-// byte offset), the next 64 channels one block on (leading byte offset).
-__device__ __forceinline__ uint64_t la_mn_desc(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(kLaBlock >> 4) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
-    return d;
+// Shared-memory descriptors of the MMAs, by their low words (address / 16 and leading byte offset / 16): the high word is
+// the same for all.  Both kinds have 128-byte swizzle and 8 rows 1024 bytes apart (stride byte offset):
+// K-major, a token's (or score row's) 128 bytes along K, as sw128_kmajor_desc; MN-major, 64 channels of a token in
+// a row, the rows along K, the next 64 channels one block on (leading byte offset).
+constexpr uint32_t kLaDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t la_k_desc(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t la_mn_desc(uint32_t saddr) { return (saddr >> 4) | ((uint32_t)(kLaBlock >> 4) << 16); }
+
+__device__ __forceinline__ void la_mma(uint32_t tmem_d, uint32_t da, uint32_t db, uint32_t idesc, bool accum) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(tmem_d),
+        "r"(da), "r"(db), "r"(idesc), "r"((uint32_t)accum), "n"(kLaDescHi)
+        : "memory");
 }
 
-// MMA with A in tensor memory (two bf16 of K per column, a row per lane).
-__device__ __forceinline__ void tc_mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t db, uint32_t idesc, uint32_t accum) {
+// The same with A in tensor memory (two bf16 of K per column, a row per lane).
+__device__ __forceinline__ void la_mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t db, uint32_t idesc, bool accum) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(tmem_d),
-        "r"(tmem_a), "l"(db), "r"(idesc), "r"(accum)
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(tmem_d),
+        "r"(tmem_a), "r"(db), "r"(idesc), "r"((uint32_t)accum), "n"(kLaDescHi)
         : "memory");
 }
 
@@ -242,20 +252,47 @@ __device__ __forceinline__ void la_zero_rows(unsigned char* v, int vb, int n, in
     }
 }
 
-// sum over j0 <= j < j1 of P[i][j] V[j][ch], from the swizzled tiles (P in two parts).  Not inlined: it is for chunks
-// that hold infinities or NaN only, and the code around it has to stay in the instruction cache.
-__device__ __noinline__ float la_dot(const unsigned char* pt, const unsigned char* vt, int i, int ch, int j0, int j1) {
-    float acc = 0.f;
-#pragma unroll 1
-    for (int j = j0; j < j1; ++j) {
-        const unsigned char* pa = pt + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2;
-        const float pw = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(pa)) +
-                         __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(pa + kLaBlock));
-        const float vv = __bfloat162float(
-            *reinterpret_cast<const __nv_bfloat16*>(vt + j * 128 + (((ch >> 3) ^ (j & 7)) << 4) + (ch & 7) * 2));
-        acc = fmaf(pw, vv, acc);
+// r += fac * s2 on fragments: a column pair's factors are those of its tokens.
+__device__ __forceinline__ void la_add_inter(uint32_t (&r)[32], const uint32_t (&s2)[32], const float2 (&fac)[8]) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const float2 y = la_fma2(fac[k >> 1], make_float2(__uint_as_float(s2[2 * k]), __uint_as_float(s2[2 * k + 1])),
+                                 make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])));
+        r[2 * k] = __float_as_uint(y.x);
+        r[2 * k + 1] = __float_as_uint(y.y);
     }
-    return acc;
+}
+
+// The outputs of 16 channels that came out not finite: a masked token may have met a zero weight.  The sum over the
+// unmasked pairs alone, from the swizzled tiles of P (two parts) and V, plus the state's part (oi: its accumulator, 0 where
+// there is none; fac: the tokens' factors).  Thread t's fragment, as tc_ld_frag_issue lays it out.  Not inlined: it is for
+// chunks with infinities or NaN only, and the code around it has to stay in the instruction cache.
+__device__ __noinline__ void la_redo(uint32_t* out, const unsigned char* pt, const unsigned char* vt, uint32_t oi, const float* fac,
+                                     int ch0, int n, int reverse) {
+    const int lane = threadIdx.x & 31, fr = lane >> 2, fc = (lane & 3) * 2;
+    uint32_t s2[32];
+    if (oi) {
+        tc_ld_frag_issue(oi, s2);
+        tc_wait_ld32(s2);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) out[e] = s2[e];
+    }
+#pragma unroll 1
+    for (int e = 0; e < 32; ++e) {
+        const int i = 8 * (e >> 2) + fc + (e & 1), ch = ch0 + fr + 8 * ((e >> 1) & 1);
+        const int j0 = reverse ? i : 0, j1 = i >= n ? 0 : reverse ? n : i + 1;
+        float acc = 0.f;
+#pragma unroll 1
+        for (int j = j0; j < j1; ++j) {
+            const unsigned char* pa = pt + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2;
+            const float pw = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(pa)) +
+                             __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(pa + kLaBlock));
+            const float vv = __bfloat162float(
+                *reinterpret_cast<const __nv_bfloat16*>(vt + j * 128 + (((ch >> 3) ^ (j & 7)) << 4) + (ch & 7) * 2));
+            acc = fmaf(pw, vv, acc);
+        }
+        out[e] = __float_as_uint(oi ? fmaf(fac[i], __uint_as_float(out[e]), acc) : acc);
+    }
 }
 
 template <int DK, int DV, bool Y>
@@ -265,19 +302,18 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
-    // decay tables of the epilogue's and the scores' warps, one each: the warps are at different items
-    __shared__ __align__(16) float tab[6][kLaTok];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* kt = smem + NST * Cfg::StageBytes;
     unsigned char* pbuf = kt + Cfg::KtBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(pbuf + Cfg::PBytes);
+    float* tab = reinterpret_cast<float*>(pbuf + Cfg::PBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<unsigned char*>(tab) + Cfg::TabBytes);
     uint64_t* empty = full + NST;
     uint64_t* qk_full = empty + NST;   // [2]
     uint64_t* qk_empty = qk_full + 2;  // [2]
-    uint64_t* p_full = qk_empty + 2;
-    uint64_t* p_empty = p_full + 1;
-    uint64_t* kt_full = p_empty + 1;   // [NST]: one phase per chunk, whether or not its keys are needed
+    uint64_t* p_full = qk_empty + 2;   // [2]
+    uint64_t* p_empty = p_full + 2;    // [2]
+    uint64_t* kt_full = p_empty + 2;   // [NST]: one phase per chunk, whether or not its keys are needed
     uint64_t* kv_full = kt_full + NST;
     uint64_t* s_full = kv_full + 1;
     uint64_t* qs_done = s_full + 1;
@@ -286,7 +322,8 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
 
     const LaPass& p = L.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    float* wtab = tab[warp >= 8 && warp < 14 ? warp - 8 : 0];
+    // decay tables of the epilogue's and the scores' warps, one each: the warps are at different items
+    float* wtab = tab + (warp >= 8 && warp < 14 ? warp - 8 : 0) * kLaTok;
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 1);
@@ -296,9 +333,9 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         for (int i = 0; i < 2; ++i) {
             mbar_init(&qk_full[i], 1);
             mbar_init(&qk_empty[i], 64);
+            mbar_init(&p_full[i], 64);
+            mbar_init(&p_empty[i], 4);
         }
-        mbar_init(p_full, 64);
-        mbar_init(p_empty, 4);
         mbar_init(kv_full, 1);
         mbar_init(s_full, 256);
         mbar_init(qs_done, 1);
@@ -352,27 +389,26 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         // ------------------------------------------------------------------ MMA issuer
         constexpr uint32_t kDesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);  // fp32 += bf16 bf16, M 128
         constexpr uint32_t kMnA = 1u << 15, kMnB = 1u << 16;
-        const uint32_t n_tok = (uint32_t)(L.n16 >> 3) << 17, n_dk = (uint32_t)(DK >> 3) << 17;
-        const int tok_steps = L.n16 >> 4;
-        const uint64_t dq = sw128_kmajor_desc(smem_addr(smem)), dk = sw128_kmajor_desc(smem_addr(smem + Cfg::QBytes));
-        const uint64_t dv = la_mn_desc(smem_addr(smem + Cfg::QBytes + Cfg::KBytes));
-        const uint64_t dkt = la_mn_desc(smem_addr(kt)), dp = sw128_kmajor_desc(smem_addr(pbuf));
+        constexpr uint32_t n_tok = (uint32_t)(kLaTok >> 3) << 17, n_dk = (uint32_t)(DK >> 3) << 17;
+        const uint32_t dq = la_k_desc(smem_addr(smem)), dk = la_k_desc(smem_addr(smem + Cfg::QBytes));
+        const uint32_t dv = la_mn_desc(smem_addr(smem + Cfg::QBytes + Cfg::KBytes));
+        const uint32_t dkt = la_mn_desc(smem_addr(kt)), dp = la_k_desc(smem_addr(pbuf));
         uint32_t total = 0;
         for (int work = blockIdx.x; work < L.nwork; work += gridDim.x) {
             const LaItem it = la_item<Y>(L, work);
             total += (uint32_t)(it.b - it.a);
         }
-        auto stage_off = [&](uint32_t pos) { return (uint64_t)((uint32_t)((pos % NST) * Cfg::StageBytes) >> 4); };
+        auto stage_off = [&](uint32_t pos) { return (pos % NST) * (uint32_t)(Cfg::StageBytes >> 4); };
         // scores of the chunk at `pos`, whose tiles have landed
         auto scores = [&](uint32_t pos) -> bool {
             if (!la_wait(&qk_empty[pos & 1], ((pos >> 1) & 1u) ^ 1u)) return false;
             tc_fence_after();
             if (elect_one()) {
-                const uint64_t so = stage_off(pos);
+                const uint32_t so = stage_off(pos), a = dq + so, b = dk + so, d = tmem + Cfg::QK + (pos & 1) * 64;
 #pragma unroll
                 for (int kk = 0; kk < DK / 16; ++kk) {
-                    const uint64_t o = so + (uint64_t)(((kk >> 2) * kLaBlock + (kk & 3) * 32) >> 4);
-                    tc_mma(tmem + Cfg::QK + (pos & 1) * 64, dq + o, dk + o, kDesc | n_tok, kk > 0);
+                    const uint32_t o = ((kk >> 2) * kLaBlock + (kk & 3) * 32) >> 4;
+                    la_mma(d, a + o, b + o, kDesc | n_tok, kk > 0);
                 }
                 tc_commit(&qk_full[pos & 1]);
             }
@@ -385,7 +421,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
             for (int c = it.a; c < it.b && ok; ++c, ++pos) {
                 const bool has = it.in || c > it.a, need = c < it.b - 1 || it.out;
                 const int st = pos % NST;
-                const uint64_t so = stage_off(pos);
+                const uint32_t so = stage_off(pos);
                 if (!(ok = la_wait(&full[st], (pos / NST) & 1u))) break;
                 if (Y && nqk == pos) {
                     if (!(ok = scores(pos))) break;
@@ -399,10 +435,9 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                         for (int part = 0; part < 3; ++part)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                if (part < L.nsplit && kk < tok_steps)
-                                    tc_mma(tmem + Cfg::KV, dv + so + (uint64_t)(kk * 2048 >> 4),
-                                           dkt + (uint64_t)((part * Cfg::KBytes + kk * 2048) >> 4), kDesc | kMnA | kMnB | n_dk,
-                                           part > 0 || kk > 0);
+                                if (part < 2 || L.nsplit > 2)
+                                    la_mma(tmem + Cfg::KV, dv + so + (kk * 2048 >> 4), dkt + ((part * Cfg::KBytes + kk * 2048) >> 4),
+                                           kDesc | kMnA | kMnB | n_dk, part > 0 || kk > 0);
                         tc_commit(kv_full);
                         if (!Y) tc_commit(&empty[st]);
                     }
@@ -424,24 +459,24 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                             for (int part = 0; part < 2; ++part)
 #pragma unroll
                                 for (int kk = 0; kk < DK / 16; ++kk)
-                                    tc_mma_ts(tmem + Cfg::OI, tmem + Cfg::SB + part * (DK / 2) + kk * 8,
-                                              dq + so + (uint64_t)(((kk >> 2) * kLaBlock + (kk & 3) * 32) >> 4), kDesc | n_tok,
+                                    la_mma_ts(tmem + Cfg::OI, tmem + Cfg::SB + part * (DK / 2) + kk * 8,
+                                              dq + so + (((kk >> 2) * kLaBlock + (kk & 3) * 32) >> 4), kDesc | n_tok,
                                               part > 0 || kk > 0);
                             tc_commit(qs_done);
                         }
                         __syncwarp();
                         ++nqs;
                     }
-                    if (!(ok = la_wait(p_full, pos & 1u))) break;
+                    if (!(ok = la_wait(&p_full[pos & 1], (pos >> 1) & 1u))) break;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                if (kk < tok_steps)
-                                    tc_mma(tmem + Cfg::OA, dv + so + (uint64_t)(kk * 2048 >> 4),
-                                           dp + (uint64_t)((part * kLaBlock + kk * 32) >> 4), kDesc | kMnA | n_tok, part > 0 || kk > 0);
+                                la_mma(tmem + Cfg::OA, dv + so + (kk * 2048 >> 4),
+                                       dp + (pos & 1) * (Cfg::PPart * 2 >> 4) + ((part * Cfg::PPart + kk * 32) >> 4),
+                                       kDesc | kMnA | n_tok, part > 0 || kk > 0);
                         tc_commit(o_full);
                         tc_commit(&empty[st]);
                     }
@@ -622,79 +657,75 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                 if (!(ok = la_wait(o_full, pos & 1u))) break;
                 tc_fence_after();
                 unsigned char* tile = smem + st * Cfg::StageBytes + quarter * (kLaBlock / 2);
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {  // channels c0 + 16 half ..
-                    uint32_t r[32], s2[32];
-                    if (used) {
+                // channels c0 + 16 half ..; bf16 results wait in w until the accumulators are given back
+                uint32_t w[2][16];
+                if (used) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t r[32], s2[32];
                         const uint32_t ta = tmem + lane_off + ((uint32_t)(half * 16) << 16);
                         tc_ld_frag_issue(ta + Cfg::OA, r);
                         if (has) tc_ld_frag_issue(ta + Cfg::OI, s2);
                         tc_wait_ld32(r);
-                        if (has) tc_wait_ld32(s2);
-                        auto add_inter = [&] {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const float2 y = la_fma2(fac[k >> 1], make_float2(__uint_as_float(s2[2 * k]), __uint_as_float(s2[2 * k + 1])),
-                                                         make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])));
-                                r[2 * k] = __float_as_uint(y.x);
-                                r[2 * k + 1] = __float_as_uint(y.y);
-                            }
-                        };
-                        if (has) add_inter();
+                        if (has) {
+                            tc_wait_ld32(s2);
+                            la_add_inter(r, s2, fac);
+                        }
                         uint32_t big = 0;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (8 * (k >> 1) < L.n16)
-                                big = la_absmax_bf16x2(big, pack_bf16x2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])));
-                        if (__any_sync(0xffffffffu, la_not_finite(big))) {
-                            // a masked token may have met a zero weight: the sums over the unmasked pairs alone
-                            la_wait(p_full, pos & 1u);
-                            la_wait(&full[st], (pos / NST) & 1u);
-                            const unsigned char* vt = smem + st * Cfg::StageBytes + Cfg::QBytes + Cfg::KBytes + (c0 >> 6) * kLaBlock;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int i = 8 * (e >> 2) + fc + (e & 1), ch = (c0 & 63) + half * 16 + fr + 8 * ((e >> 1) & 1);
-                                const int j0 = p.reverse ? i : 0, j1 = i >= n ? 0 : p.reverse ? n : i + 1;
-                                r[e] = __float_as_uint(la_dot(pbuf, vt, i, ch, j0, j1));
-                            }
-                            if (has) add_inter();
+                        for (int k = 0; k < 16; ++k) {
+                            w[half][k] = pack_bf16x2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+                            big = la_absmax_bf16x2(big, w[half][k]);
                         }
-                        if (n != kLaTok) {  // rows past the length are stored as zeros (past seq_len: not at all)
+                        const bool redo = __any_sync(0xffffffffu, la_not_finite(big));
+                        if (redo || n != kLaTok || p.y_f32) {
+                            if (redo) {
+                                la_wait(&p_full[pos & 1], (pos >> 1) & 1u);
+                                la_wait(&full[st], (pos / NST) & 1u);
+                                uint32_t again[32];
+                                la_redo(again, pbuf + (pos & 1) * 2 * Cfg::PPart,
+                                        smem + st * Cfg::StageBytes + Cfg::QBytes + Cfg::KBytes + (c0 >> 6) * kLaBlock,
+                                        has ? ta + Cfg::OI : 0u, wtab, (c0 & 63) + half * 16, n, p.reverse);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
+                                for (int e = 0; e < 32; ++e) r[e] = again[e];
+                            }
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)  // rows past the length are stored as zeros (past seq_len: not at all)
                                 if (8 * (e >> 2) + fc + (e & 1) >= n) r[e] = 0u;
-                        }
-                    }
-                    if (half == 1) {
-                        // both accumulators, P and V have been read
-                        tc_fence_before();
-                        mbar_arrive(o_empty);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(p_empty);
-                    }
-                    if (used) {
-                        if (p.y_f32) {
-                            float* y = static_cast<float*>(p.y) + ((size_t)it.seq * p.seq_len + row0) * p.y_tok + (size_t)it.h * p.dv;
+                            if (p.y_f32) {
+                                float* y = static_cast<float*>(p.y) + ((size_t)it.seq * p.seq_len + row0 + fc) * p.y_tok +
+                                           (size_t)it.h * p.dv + c0 + half * 16 + fr;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int i = 8 * (e >> 2) + fc + (e & 1), ch = c0 + half * 16 + fr + 8 * ((e >> 1) & 1);
-                                if (row0 + i < p.seq_len && ch < p.dv) y[(size_t)i * p.y_tok + ch] = __uint_as_float(r[e]);
-                            }
-                        } else {
-                            // [token][32 channels], 64-byte rows, 16-byte pieces swizzled by the row pair
-                            const uint32_t ts = smem_addr(tile);
-                            const int tr = lane & 7, m = half * 2 + ((lane >> 3) & 1);
+                                for (int k = 0; k < 8; ++k, y += 8 * p.y_tok)
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const int i = 8 * k + tr;
-                                st_matrix2_trans(ts + i * 64 + ((m ^ ((i >> 1) & 3)) << 4),
-                                                 pack_bf16x2(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1])),
-                                                 pack_bf16x2(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3])));
+                                    for (int e = 0; e < 4; ++e)
+                                        if (row0 + 8 * k + fc + (e & 1) < p.seq_len && c0 + half * 16 + fr + 8 * (e >> 1) < p.dv)
+                                            y[(e & 1) * p.y_tok + 8 * (e >> 1)] = __uint_as_float(r[4 * k + e]);
                             }
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                w[half][k] = pack_bf16x2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
                         }
                     }
                 }
+                // both accumulators, P and V have been read
+                tc_fence_before();
+                mbar_arrive(o_empty);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_empty[pos & 1]);
                 if (used && !p.y_f32) {
+                    // [token][32 channels], 64-byte rows, 16-byte pieces swizzled by the row pair
+                    const uint32_t ts = smem_addr(tile);
+                    const int tr = lane & 7;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int m = half * 2 + ((lane >> 3) & 1);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int i = 8 * k + tr;
+                            st_matrix2_trans(ts + i * 64 + ((m ^ ((i >> 1) & 3)) << 4), w[half][2 * k], w[half][2 * k + 1]);
+                        }
+                    }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) {
@@ -722,14 +753,14 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         // ------------------------------------------------------------------ scores
         const int w = warp - 12, i = 32 * w + lane;  // the row (token) of this thread
         const uint32_t lane_off = (uint32_t)(32 * w) << 16;
-        unsigned char* pb = pbuf + i * 128;
+        unsigned char* const prow = pbuf + i * 128;
         // of the two blocks off the diagonal one is all masked: it stays zero
         const bool full_block = p.reverse ? w == 0 : w == 1;
 #pragma unroll
         for (int q = 0; q < 8; ++q)
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
-                *reinterpret_cast<uint4*>(pb + part * kLaBlock + q * 16) = make_uint4(0, 0, 0, 0);
+            for (int part = 0; part < 4; ++part)
+                *reinterpret_cast<uint4*>(prow + part * Cfg::PPart + q * 16) = make_uint4(0, 0, 0, 0);
         __syncwarp();
         const float s = p.s_in * p.s_out;
         uint32_t pos = 0;
@@ -756,6 +787,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                 if (!(ok = la_wait(&qk_full[pos & 1], (pos >> 1) & 1u))) break;
                 tc_fence_after();
                 const uint32_t ta = tmem + lane_off + Cfg::QK + (pos & 1) * 64;
+                unsigned char* pb = prow + (pos & 1) * 2 * Cfg::PPart;
                 uint32_t r[32];
                 // 32 scores of this row, weighted, in two bf16 parts, to columns c0 .. c0 + 31 of P
                 auto put = [&](int col0, const float2 (&wt)[16]) {
@@ -776,9 +808,9 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                 };
                 tc_ld32_issue(ta + 32 * w, r);
                 tc_wait_ld32(r);
-                if (!(ok = la_wait(p_empty, (pos & 1u) ^ 1u))) break;
+                if (!(ok = la_wait(&p_empty[pos & 1], ((pos >> 1) & 1u) ^ 1u))) break;
                 put(32 * w, wd);
-                if (full_block && L.n16 > 32) {
+                if (full_block && n > 32) {
                     tc_ld32_issue(ta + 32 * (1 - w), r);
                     tc_wait_ld32(r);
                     put(32 * (1 - w), wo);
@@ -791,7 +823,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     la_zero_rows(smem + st * Cfg::StageBytes + Cfg::QBytes + Cfg::KBytes, Cfg::VB, n, i, 64);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive(p_full);
+                mbar_arrive(&p_full[pos & 1]);
             }
         }
     }
@@ -907,7 +939,6 @@ inline bool linattn_tc_launch(const LaPass& p, float* seg, int nsm, cudaStream_t
     L.seg = seg;
     la_segments(p.nseq, p.heads, p.seq_len, nsm, L.nseg, L.seg_chunks);
     L.box_rows = std::min(kLaTok, (p.seq_len + 7) & ~7);
-    L.n16 = (L.box_rows + 15) & ~15;
     L.nsplit = p.h_last ? 3 : 2;
     if (!la_encode(&L.tq, p.q, p.dk, p.heads / p.q_div, p.seq_len, p.nseq, p.q_tok, L.box_rows) ||
         !la_encode(&L.tk, p.k, p.dk, p.heads / p.k_div, p.seq_len, p.nseq, p.k_tok, L.box_rows) ||
