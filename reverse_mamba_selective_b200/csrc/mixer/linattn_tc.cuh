@@ -156,6 +156,19 @@ __device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || la_wait_long(bar, parity);
 }
 
+// Whether the phase with the given parity has completed; never suspends the warp (try_wait may, for microseconds).
+__device__ __forceinline__ bool la_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, ok != 0);
+}
+
 // One (sequence, head, segment): chunks a .. b - 1 in scan order of the nch chunks of its sequence.
 struct LaItem {
     int seq, h, len, nch, a, b;
@@ -234,10 +247,10 @@ __device__ __forceinline__ uint32_t la_split(float2& x) {
     return w;
 }
 
-// max(|m|, |w|) of the bf16 halves, NaN if either is.
+// max(|m|, |w|) of the bf16 halves but for the sign, NaN if either is.
 __device__ __forceinline__ uint32_t la_absmax_bf16x2(uint32_t m, uint32_t w) {
     uint32_t d;
-    asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %2;\n\tmax.NaN.bf16x2 %0, %1, a;\n\t}\n" : "=r"(d) : "r"(m), "r"(w));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w));
     return d;
 }
 __device__ __forceinline__ bool la_not_finite(uint32_t m) { return (m & 0x7F80u) == 0x7F80u || (m & 0x7F800000u) == 0x7F800000u; }
@@ -445,8 +458,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                 }
                 if (Y) {
                     // the next chunk's scores early, if its tiles are there
-                    if (pos + 1 < total &&
-                        __all_sync(0xffffffffu, mbar_try_wait(&full[(pos + 1) % NST], ((pos + 1) / NST) & 1u))) {
+                    if (pos + 1 < total && la_test(&full[(pos + 1) % NST], ((pos + 1) / NST) & 1u)) {
                         if (!(ok = scores(pos + 1))) break;
                         nqk = pos + 2;
                     }
