@@ -1,6 +1,7 @@
 // mixer.cu -- host side of libr2l_mixer: argument validation, kernel choice and the extern "C" entry points
 // declared in include/r2l_mixer.h.  Single translation unit, as libr2l.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstdint>
 #include <cstring>
@@ -23,10 +24,14 @@ inline int esize(r2l_dtype t) { return t == R2L_BF16 ? 2 : 4; }
 inline bool valid_dtype(r2l_dtype t) { return t == R2L_F32 || t == R2L_BF16; }
 inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
+// SMs of the current device (asked once per device).
 int sm_count() {
+    static std::atomic<int> known[64];
     int dev = 0, v = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (dev >= 0 && dev < 64 && (v = known[dev].load(std::memory_order_relaxed)) > 0) return v;
     if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) return 148;
+    if (dev >= 0 && dev < 64) known[dev].store(v, std::memory_order_relaxed);
     return v;
 }
 

@@ -8,7 +8,6 @@ and there is no CPU fallback.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Dict, Optional, Tuple
@@ -111,22 +110,27 @@ def _raise(st: int, where: str):
         raise MixerError(st, where)
 
 
-def _on_device(t: torch.Tensor):
+class _Here:
+    """Nothing to switch: the tensors' device is the current one."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on_device(index: int):
     """The tensors' device made current: the library works on the current device."""
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+    return _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
-def _same_device(dev: torch.device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
-
-
-def _stream_of(stream, *made):
+def _stream_of(stream, index: int, *made):
     """The raw stream; tensors made here that another stream than the current one works on are tied to it."""
-    cur = torch.cuda.current_stream().cuda_stream
+    cur = torch._C._cuda_getCurrentRawStream(index)
     if stream is None:
         return cur
     raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -137,60 +141,87 @@ def _stream_of(stream, *made):
     return raw
 
 
-def _heads(name: str, t: torch.Tensor, dtype, batch: int, seqlen: int) -> int:
-    """Checks a [batch, seqlen, heads, d] operand (heads and channels dense, tokens evenly spaced) and returns its
-    elements from token to token."""
+def _ptr_of(name: str, t: Optional[torch.Tensor], dtype, shape, index: int) -> Optional[int]:
+    """The address of an optional dense tensor of the given type, shape (None: any) and device."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        _check_dev(name, t, dtype, shape)  # says what is wrong
+    if t.get_device() != index:
+        raise (ValueError if t.is_cuda else TypeError)(f"{name} must be on cuda:{index}, got {t.device}")
+    return t.data_ptr()
+
+
+def _first(name: str, t, dims: int) -> int:
+    """The CUDA device of the first operand, which has to have a supported type and ``dims`` dimensions."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
+    if t.dtype not in _DTYPE_CODE:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return t.get_device()
+
+
+def _heads(name: str, t: torch.Tensor, dtype, lead: Tuple[int, ...], index: int) -> int:
+    """Checks a [*lead, heads, d] operand (heads and channels dense, tokens evenly spaced over lead) and returns its
+    elements from token to token (0: dense)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 4 or t.shape[0] != batch or t.shape[1] != seqlen:
-        raise ValueError(f"{name} must have shape [{batch}, {seqlen}, heads, d], got {tuple(t.shape)}")
-    sb, sl, sh, sd = t.stride()
-    heads, d = t.shape[2], t.shape[3]
-    if (d > 1 and sd != 1) or (heads > 1 and sh != d):
+    shape = t.shape
+    if len(shape) != len(lead) + 2 or shape[:-2] != lead:
+        raise ValueError(f"{name} must have shape [{', '.join(map(str, lead))}, heads, d], got {tuple(shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    if t.is_contiguous():
+        return 0
+    strides = t.stride()
+    heads, d = shape[-2], shape[-1]
+    if (d > 1 and strides[-1] != 1) or (heads > 1 and strides[-2] != d):
         raise ValueError(f"{name} must have dense heads and channels")
-    tok = sl if seqlen > 1 else (sb if batch > 1 else heads * d)
-    if t.numel() == 0:
-        return heads * d
-    if tok < heads * d or (seqlen > 1 and batch > 1 and sb != seqlen * sl):
-        raise ValueError(f"{name} must have its tokens evenly spaced over batch and sequence")
+    # the innermost dimension of lead that has more than one entry gives the tokens' distance, the others follow from it
+    tok, want = 0, 0
+    for n, st in zip(reversed(lead), reversed(strides[:-2])):
+        if want == 0:
+            if n > 1:
+                tok, want = st, st * n
+            continue
+        if n > 1 and st != want:
+            raise ValueError(f"{name} must have its tokens evenly spaced")
+        want *= n
+    if tok and tok < heads * d:
+        raise ValueError(f"{name} must not have overlapping tokens")
     return tok
 
 
-def _linattn_args(q, k, v, log_decay, scale, block_len, reverse, seq_lens) -> LinattnArgs:
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must have shape [batch, seqlen, heads, d_k]")
+def _linattn_args(q, k, v, log_decay, scale, block_len, reverse, seq_lens, lead, index) -> LinattnArgs:
     dtype = q.dtype
-    if dtype not in _DTYPE_CODE:
-        raise TypeError(f"unsupported dtype {dtype}")
-    batch, seqlen = q.shape[0], q.shape[1]
-    qs, ks, vs = (_heads(n, t, dtype, batch, seqlen) for n, t in (("q", q), ("k", k), ("v", v)))
-    if k.shape[3] != q.shape[3]:
+    qs, ks, vs = _heads("q", q, dtype, lead, index), _heads("k", k, dtype, lead, index), _heads("v", v, dtype, lead, index)
+    batch, seqlen = lead if len(lead) == 2 else (lead[0], 1)
+    d_k = q.shape[-1]
+    if k.shape[-1] != d_k:
         raise ValueError("q and k must have the same head size")
-    _check_dev("log_decay", log_decay, torch.float32)
-    if log_decay.dim() != 1:
+    if isinstance(log_decay, torch.Tensor) and log_decay.dim() != 1:
         raise ValueError("log_decay must have shape [heads]")
-    _check_dev("seq_lens", seq_lens, torch.int32, (batch,))
-    _same_device(q.device, k=k, v=v, log_decay=log_decay, seq_lens=seq_lens)
-    d_k = q.shape[3]
+    decay = _ptr_of("log_decay", log_decay, torch.float32, None, index)
+    lens = _ptr_of("seq_lens", seq_lens, torch.int32, (batch,), index)
     if scale is None:
         scale = d_k ** -0.5 if d_k else 1.0
-    return LinattnArgs(batch, seqlen, seqlen if block_len is None else int(block_len), log_decay.shape[0], q.shape[2],
-                       k.shape[2], v.shape[2], d_k, v.shape[3], int(bool(reverse)), _DTYPE_CODE[dtype], float(scale),
-                       _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(log_decay), _ptr(seq_lens))
+    return LinattnArgs(batch, seqlen, seqlen if block_len is None else int(block_len), log_decay.shape[0], q.shape[-2],
+                       k.shape[-2], v.shape[-2], d_k, v.shape[-1], 1 if reverse else 0, _DTYPE_CODE[dtype], scale,
+                       q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, decay, lens)
 
 
-def _workspace(given: Optional[torch.Tensor], need: int, device) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], int]:
-    """(workspace or None, the one made here or None, its bytes)."""
+def _workspace(given: Optional[torch.Tensor], need: int, like: torch.Tensor, index: int):
+    """(address or None, the tensor made here or None, bytes)."""
     if given is not None:
-        _check_dev("workspace", given)
-        _same_device(device, workspace=given)
-        return given, None, given.numel() * given.element_size()
+        return _ptr_of("workspace", given, given.dtype, None, index), None, given.numel() * given.element_size()
     if need == 0:
         return None, None, 0
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    return ws, ws, need
+    ws = like.new_empty(need, dtype=torch.uint8)
+    return ws.data_ptr(), ws, need
 
 
 def r2l_linattn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
@@ -207,22 +238,26 @@ def r2l_linattn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: to
     Returns (y [b, L, heads, d_v], h_last or None).
     """
     lib = load_mixer()
-    a = _linattn_args(q, k, v, log_decay, scale, block_len, reverse, seq_lens)
+    index = _first("q", q, 4)
+    a = _linattn_args(q, k, v, log_decay, scale, block_len, reverse, seq_lens, tuple(q.shape[:2]), index)
     state = (a.batch, a.n_heads, a.d_k, a.d_v)
-    _check_dev("h0", h0, torch.float32, state)
-    _check_dev("h_last", h_last, torch.float32, state)
     shape = (a.batch, a.seqlen, a.n_heads, a.d_v)
-    _check_dev("y", y, q.dtype, shape)
-    _same_device(q.device, h0=h0, h_last=h_last, y=y)
-    with _on_device(q):
+    p0 = _ptr_of("h0", h0, torch.float32, state, index)
+    p1 = _ptr_of("h_last", h_last, torch.float32, state, index)
+    py = _ptr_of("y", y, q.dtype, shape, index)
+    ref = ctypes.byref(a)
+    with _on_device(index):
         made_h = made_y = None
         if h_last is None and want_h_last:
-            h_last = made_h = torch.empty(state, dtype=torch.float32, device=q.device)
+            h_last = made_h = q.new_empty(state, dtype=torch.float32)
+            p1 = h_last.data_ptr()
         if y is None:
-            y = made_y = torch.empty(shape, dtype=q.dtype, device=q.device)
-        ws, made, nbytes = _workspace(workspace, int(lib.r2l_linattn_workspace_size(ctypes.byref(a))), q.device)
-        _raise(lib.r2l_linattn(ctypes.byref(a), _ptr(h0), _ptr(h_last), _ptr(y), _ptr(ws), nbytes,
-                               _stream_of(stream, made_h, made_y, made)), "r2l_linattn")
+            y = made_y = q.new_empty(shape)
+            py = y.data_ptr()
+        ws, made, nbytes = _workspace(workspace, lib.r2l_linattn_workspace_size(ref), q, index)
+        st = lib.r2l_linattn(ref, p0, p1, py, ws, nbytes, _stream_of(stream, index, made_h, made_y, made))
+    if st != R2L_OK:
+        _raise(st, "r2l_linattn")
     return y, h_last
 
 
@@ -232,24 +267,24 @@ def r2l_linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     """One token of every sequence: q [b, q_heads, d_k], k [b, k_heads, d_k], v [b, v_heads, d_v], state h
     [b, heads, d_k, d_v] fp32, updated in place unless ``h_out`` is given.  Returns y [b, heads, d_v]."""
     lib = load_mixer()
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 3:
-            raise ValueError(f"{name} must have shape [batch, heads, d]")
-    a = _linattn_args(q.unsqueeze(1), k.unsqueeze(1), v.unsqueeze(1), log_decay, scale, None, False, None)
+    index = _first("q", q, 3)
+    a = _linattn_args(q, k, v, log_decay, scale, None, False, None, (q.shape[0],), index)
     state = (a.batch, a.n_heads, a.d_k, a.d_v)
+    shape = (a.batch, a.n_heads, a.d_v)
     if h is None:
         raise ValueError("h must be given")
-    _check_dev("h", h, torch.float32, state)
-    _check_dev("h_out", h_out, torch.float32, state)
-    shape = (a.batch, a.n_heads, a.d_v)
-    _check_dev("y", y, q.dtype, shape)
-    _same_device(q.device, h=h, h_out=h_out, y=y)
-    with _on_device(q):
+    p0 = p1 = _ptr_of("h", h, torch.float32, state, index)
+    if h_out is not None:
+        p1 = _ptr_of("h_out", h_out, torch.float32, state, index)
+    py = _ptr_of("y", y, q.dtype, shape, index)
+    with _on_device(index):
         made = None
         if y is None:
-            y = made = torch.empty(shape, dtype=q.dtype, device=q.device)
-        _raise(lib.r2l_linattn_step(ctypes.byref(a), _ptr(h), _ptr(h if h_out is None else h_out), _ptr(y),
-                                    _stream_of(stream, made)), "r2l_linattn_step")
+            y = made = q.new_empty(shape)
+            py = y.data_ptr()
+        st = lib.r2l_linattn_step(ctypes.byref(a), p0, p1, py, _stream_of(stream, index, made))
+    if st != R2L_OK:
+        _raise(st, "r2l_linattn_step")
     return y
 
 
@@ -264,69 +299,52 @@ def r2l_linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
     given, else None).
     """
     lib = load_mixer()
-    a = _linattn_args(q, k, v, log_decay, scale, block_len, reverse, seq_lens)
+    index = _first("q", q, 4)
+    a = _linattn_args(q, k, v, log_decay, scale, block_len, reverse, seq_lens, tuple(q.shape[:2]), index)
     state = (a.batch, a.n_heads, a.d_k, a.d_v)
     if dy is None:
         raise ValueError("dy must be given")
-    _check_dev("dy", dy, q.dtype, (a.batch, a.seqlen, a.n_heads, a.d_v))
-    _check_dev("h0", h0, torch.float32, state)
-    _check_dev("dh_last", dh_last, torch.float32, state)
-    _same_device(q.device, dy=dy, h0=h0, dh_last=dh_last)
+    pdy = _ptr_of("dy", dy, q.dtype, (a.batch, a.seqlen, a.n_heads, a.d_v), index)
+    p0 = _ptr_of("h0", h0, torch.float32, state, index)
+    pdh = _ptr_of("dh_last", dh_last, torch.float32, state, index)
     if want_dh0 is None:
         want_dh0 = h0 is not None
-    with _on_device(q):
-        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
-        dh0 = torch.empty(state, dtype=torch.float32, device=q.device) if want_dh0 else None
-        ws, made, nbytes = _workspace(workspace, int(lib.r2l_linattn_bwd_workspace_size(ctypes.byref(a))), q.device)
-        _raise(lib.r2l_linattn_bwd(ctypes.byref(a), _ptr(dy), _ptr(h0), _ptr(dh_last), _ptr(dq), _ptr(dk), _ptr(dv),
-                                   _ptr(dh0), _ptr(ws), nbytes, _stream_of(stream, dq, dk, dv, dh0, made)),
-               "r2l_linattn_bwd")
+    ref = ctypes.byref(a)
+    with _on_device(index):
+        dq, dk, dv = q.new_empty(q.shape), q.new_empty(k.shape), q.new_empty(v.shape)
+        dh0 = q.new_empty(state, dtype=torch.float32) if want_dh0 else None
+        ws, made, nbytes = _workspace(workspace, lib.r2l_linattn_bwd_workspace_size(ref), q, index)
+        st = lib.r2l_linattn_bwd(ref, pdy, p0, pdh, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dh0), ws, nbytes,
+                                 _stream_of(stream, index, dq, dk, dv, dh0, made))
+    if st != R2L_OK:
+        _raise(st, "r2l_linattn_bwd")
     return {"dq": dq, "dk": dk, "dv": dv, "dh0": dh0}
 
 
 # ----------------------------------------------------------------------------- norm and rotation
 
-def _tokens(name: str, t: torch.Tensor, dtype, tokens: int, dim: int) -> int:
-    """Checks a [tokens, heads, dim] operand and returns its elements from token to token."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != dim:
-        raise ValueError(f"{name} must have shape [{tokens}, heads, {dim}], got {tuple(t.shape)}")
-    st, sh, sd = t.stride()
-    heads = t.shape[1]
-    if t.numel() == 0 or tokens == 1:
-        st = heads * dim
-    if (dim > 1 and sd != 1) or (heads > 1 and sh != dim) or st < heads * dim:
-        raise ValueError(f"{name} must have dense heads and channels and tokens that do not overlap")
-    return st
-
-
-def _rope_args(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved) -> QkNormRopeArgs:
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must have shape [tokens, heads, head_dim]")
-    if q.dtype not in _DTYPE_CODE:
-        raise TypeError(f"unsupported dtype {q.dtype}")
-    tokens, _, dim = q.shape
-    qs, ks = _tokens("q", q, q.dtype, tokens, dim), _tokens("k", k, q.dtype, tokens, dim)
-    _check_dev("q_weight", q_weight, torch.float32, (dim,))
-    _check_dev("k_weight", k_weight, torch.float32, (dim,))
-    rot = 0
+def _rope_args(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, index) -> QkNormRopeArgs:
+    dtype = q.dtype
+    tokens, q_heads, dim = q.shape
+    qs, ks = _heads("q", q, dtype, (tokens,), index), _heads("k", k, dtype, (tokens,), index)
+    if k.shape[2] != dim:
+        raise ValueError("q and k must have the same head size")
+    wq = _ptr_of("q_weight", q_weight, torch.float32, (dim,), index)
+    wk = _ptr_of("k_weight", k_weight, torch.float32, (dim,), index)
+    rot, wide, pp, pf = 0, 0, None, None
     if inv_freq is not None:
-        _check_dev("inv_freq", inv_freq, torch.float32)
-        if inv_freq.dim() != 1:
+        if isinstance(inv_freq, torch.Tensor) and inv_freq.dim() != 1:
             raise ValueError("inv_freq must have shape [rot_dim / 2]")
+        pf = _ptr_of("inv_freq", inv_freq, torch.float32, None, index)
         rot = 2 * inv_freq.shape[0]
         if positions is None:
             raise ValueError("positions must be given with inv_freq")
-        if positions.dtype not in (torch.int32, torch.int64):
+        wide = 1 if positions.dtype is torch.int64 else 0
+        if not wide and positions.dtype is not torch.int32:
             raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
-        _check_dev("positions", positions, None, (tokens,))
-    _same_device(q.device, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions, inv_freq=inv_freq)
-    return QkNormRopeArgs(tokens, q.shape[1], k.shape[1], dim, rot, int(bool(interleaved)),
-                          int(positions is not None and positions.dtype == torch.int64), _DTYPE_CODE[q.dtype], float(eps),
-                          _ptr(q), _ptr(k), qs, ks, _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq))
+        pp = _ptr_of("positions", positions, positions.dtype, (tokens,), index)
+    return QkNormRopeArgs(tokens, q_heads, k.shape[1], dim, rot, 1 if interleaved else 0, wide, _DTYPE_CODE[dtype], eps,
+                          q.data_ptr(), k.data_ptr(), qs, ks, wq, wk, pp, pf)
 
 
 def r2l_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
@@ -340,21 +358,26 @@ def r2l_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.
     neighbouring channels, else channel i with i + rot / 2.  q_out may be q and k_out may be k.  Returns (q_out, k_out).
     """
     lib = load_mixer()
-    a = _rope_args(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
-    qs = _tokens("q_out", q_out, q.dtype, a.tokens, a.head_dim) if q_out is not None else 0
-    ks = _tokens("k_out", k_out, q.dtype, a.tokens, a.head_dim) if k_out is not None else 0
-    for name, o, t in (("q_out", q_out, q), ("k_out", k_out, k)):
-        if o is not None and o.shape != t.shape:
-            raise ValueError(f"{name} must have shape {tuple(t.shape)}, got {tuple(o.shape)}")
-    _same_device(q.device, q_out=q_out, k_out=k_out)
-    with _on_device(q):
-        made_q = made_k = None
+    index = _first("q", q, 3)
+    a = _rope_args(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, index)
+    qs = ks = 0
+    made_q = made_k = None
+    with _on_device(index):
         if q_out is None:
-            q_out = made_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = made_q = q.new_empty(q.shape)
+        else:
+            qs = _heads("q_out", q_out, q.dtype, (a.tokens,), index)
         if k_out is None:
-            k_out = made_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        _raise(lib.r2l_qk_norm_rope(ctypes.byref(a), _ptr(q_out), qs, _ptr(k_out), ks, _stream_of(stream, made_q, made_k)),
-               "r2l_qk_norm_rope")
+            k_out = made_k = q.new_empty(k.shape)
+        else:
+            ks = _heads("k_out", k_out, q.dtype, (a.tokens,), index)
+        for name, o, t in (("q_out", q_out, q), ("k_out", k_out, k)):
+            if o.shape != t.shape:
+                raise ValueError(f"{name} must have shape {tuple(t.shape)}, got {tuple(o.shape)}")
+        st = lib.r2l_qk_norm_rope(ctypes.byref(a), q_out.data_ptr(), qs, k_out.data_ptr(), ks,
+                                  _stream_of(stream, index, made_q, made_k))
+    if st != R2L_OK:
+        _raise(st, "r2l_qk_norm_rope")
     return q_out, k_out
 
 
@@ -366,26 +389,27 @@ def r2l_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[to
     """Gradients of r2l_qk_norm_rope (q and k: its inputs) given dq_out, dk_out: dq, dk in the inputs' type and
     dq_weight, dk_weight [d] fp32 (also where the weights were None, i.e. ones)."""
     lib = load_mixer()
-    a = _rope_args(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved)
+    index = _first("q", q, 3)
+    a = _rope_args(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, index)
     if dq_out is None or dk_out is None:
         raise ValueError("dq_out and dk_out must be given")
-    _check_dev("dq_out", dq_out, q.dtype, q.shape)
-    _check_dev("dk_out", dk_out, q.dtype, k.shape)
-    _same_device(q.device, dq_out=dq_out, dk_out=dk_out)
-    with _on_device(q):
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        dqw, dkw = (torch.empty(a.head_dim, dtype=torch.float32, device=q.device) for _ in range(2))
-        ws, made, nbytes = _workspace(workspace, int(lib.r2l_qk_norm_rope_bwd_workspace_size(ctypes.byref(a))), q.device)
-        _raise(lib.r2l_qk_norm_rope_bwd(ctypes.byref(a), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw),
-                                        _ptr(ws), nbytes, _stream_of(stream, dq, dk, dqw, dkw, made)),
-               "r2l_qk_norm_rope_bwd")
+    pdq = _ptr_of("dq_out", dq_out, q.dtype, q.shape, index)
+    pdk = _ptr_of("dk_out", dk_out, q.dtype, k.shape, index)
+    ref = ctypes.byref(a)
+    with _on_device(index):
+        dq, dk = q.new_empty(q.shape), q.new_empty(k.shape)
+        dqw, dkw = q.new_empty(a.head_dim, dtype=torch.float32), q.new_empty(a.head_dim, dtype=torch.float32)
+        ws, made, nbytes = _workspace(workspace, lib.r2l_qk_norm_rope_bwd_workspace_size(ref), q, index)
+        st = lib.r2l_qk_norm_rope_bwd(ref, pdq, pdk, dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), ws, nbytes,
+                                      _stream_of(stream, index, dq, dk, dqw, dkw, made))
+    if st != R2L_OK:
+        _raise(st, "r2l_qk_norm_rope_bwd")
     return {"dq": dq, "dk": dk, "dq_weight": dqw, "dk_weight": dkw}
 
 
 def r2l_mixer_device_status(stream=None) -> int:
     """Synchronise and read/clear this library's device status word (R2L_OK or R2L_ERR_TIMEOUT)."""
-    return int(load_mixer().r2l_mixer_device_status(_stream_of(stream)))
+    return int(load_mixer().r2l_mixer_device_status(_stream_of(stream, torch.cuda.current_device())))
 
 
 def r2l_mixer_abi_version() -> int:
