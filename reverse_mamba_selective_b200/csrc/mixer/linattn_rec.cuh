@@ -1,41 +1,57 @@
 // linattn_rec.cuh -- linear attention token by token, the state in registers: fp32 inputs, single tokens
 // (the serving step) and runs of a few tokens.
 //
-// One CTA of 256 threads owns `cols` value columns of one (sequence, head): the state slice
-// [dk][cols] lies in registers, a thread holding four neighbouring columns of every rows_par-th row.
-// Per token and state element: t = k v, t += S gamma_lo, S = S gamma_hi + t, and one FMA for q.S.
-// A group of kRecTok tokens is staged in shared memory, their row-partial outputs are summed there.
+// One CTA of 256 threads owns 4 TPR value columns of one (sequence, head): the state slice lies in registers,
+// a thread holding four neighbouring columns of every (256 / TPR)-th row.  Per token and state element: t = k v,
+// t += S gamma_lo, S = S gamma_hi + t, and one FMA for q.S; the partial outputs of a warp's rows are
+// joined by a reduce-scatter of shuffles, those of the 8 warps in shared memory, kRecTok tokens at a time (two
+// barriers), while the next tokens are on their way into registers.
 //
-// A single token is bound by the state's read and write (2 x 4 bytes an element, all of a thread's loads in
-// flight at once); runs in fp32 by the FMA pipe (4 operations an element and token).
+// Runs in fp32 are bound by the FMA pipe where (sequence, head) pairs fill the GPU (4 operations an element and token),
+// else by the latency of a token, about a hundred cycles; then the columns are spread over more CTAs.
 #pragma once
+
+#include <algorithm>
+#include <cstring>
 
 #include "linattn_common.cuh"
 
 namespace r2l {
 
 constexpr int kRecThreads = 256;
-constexpr int kRecTok = 8;       // tokens staged at once
+constexpr int kRecTok = 8;       // tokens staged at once: one a warp
 constexpr int kRecMaxD = 128;
 
-template <typename T>
-__device__ __forceinline__ void la_store(T* p, float v) {
-    *p = from_f32<T>(v);
+// Up to three passes in one launch (the gradients): blockIdx.z says which.
+struct LaPasses {
+    LaPass p[3];
+};
+
+__device__ __forceinline__ void la_store(const LaPass& p, size_t at, float v, float) {
+    (void)p.y_f32;
+    static_cast<float*>(p.y)[at] = v;
+}
+__device__ __forceinline__ void la_store(const LaPass& p, size_t at, float v, __nv_bfloat16) {
+    if (p.y_f32)
+        static_cast<float*>(p.y)[at] = v;
+    else
+        static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
 }
 
-// MAXM: rows a thread holds (ceil(dk / rows_par) <= MAXM).
-template <typename T, typename TY, int MAXM, bool SHIFT>
-__global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(LaPass p, int cols) {
-    __shared__ float sq[kRecTok][kRecMaxD], sk[kRecTok][kRecMaxD];
-    __shared__ float sv[kRecTok][kRecMaxD];
-    __shared__ __align__(16) float part[kRecTok][kRecThreads * 4];  // [token][row group][cols]
-    const int tid = threadIdx.x;
-    const int tpr = cols >> 2, rows_par = kRecThreads / tpr;
-    const bool act = tid < tpr * rows_par;
-    const int rr = tid / tpr, cq = (tid - rr * tpr) * 4;  // first row, first column (in the slice)
-    const int c0 = blockIdx.y * cols;
-    const int ncol = min(cols, p.dv - c0);                // dv and cols are multiples of 4
-    const bool col_ok = act && cq < ncol;
+template <typename T, int TPR>
+__global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_constant__ LaPasses passes) {
+    constexpr int COLS = 4 * TPR, ROWS = kRecThreads / TPR, M = kRecMaxD / ROWS, W = 32 / TPR;  // W: rows a warp holds at once
+    constexpr int J = kRecMaxD / 32, JV = (COLS + 31) / 32;
+    __shared__ float2 sqk[kRecTok][kRecMaxD];
+    __shared__ __align__(16) float sv[kRecTok][COLS];
+    __shared__ __align__(16) float part[kRecTok][kRecThreads / 32][COLS];
+    const LaPass& p = passes.p[blockIdx.z];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rr = tid / TPR, cq = (tid % TPR) * 4;  // first row, first column (in the slice)
+    const int c0 = blockIdx.y * COLS;
+    if (c0 >= p.dv) return;  // a pass with fewer slices than another
+    const int ncol = min(COLS, p.dv - c0);           // a multiple of 4
+    const bool col_ok = cq < ncol;
     pdl_trigger();
     pdl_wait();
 
@@ -46,13 +62,13 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(LaPass p, int 
     const T* q = static_cast<const T*>(p.q) + tok0 * p.q_tok + (size_t)(h / p.q_div) * p.dk;
     const T* k = static_cast<const T*>(p.k) + tok0 * p.k_tok + (size_t)(h / p.k_div) * p.dk;
     const T* v = static_cast<const T*>(p.v) + tok0 * p.v_tok + (size_t)(h / p.v_div) * p.dv + c0;
-    TY* y = static_cast<TY*>(p.y) + tok0 * p.y_tok + (size_t)h * p.dv + c0;
+    const size_t y0 = tok0 * p.y_tok + (size_t)h * p.dv + c0;
 
     const size_t sbase = (size_t)item * p.dk * p.dv;
-    float4 s[MAXM];
+    float4 s[M];
 #pragma unroll
-    for (int m = 0; m < MAXM; ++m) {
-        const int r = rr + m * rows_par;
+    for (int m = 0; m < M; ++m) {
+        const int r = rr + m * ROWS;
         s[m] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p.h0 && col_ok && r < p.dk) {
             if (!p.h_t) {
@@ -63,75 +79,104 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(LaPass p, int 
             }
         }
     }
+    // the values of this warp's token of the group that begins at n0 (zeros past the end)
+    float fq[J], fk[J], fv[JV];
+    auto fetch = [&](int n0) {
+        const int n = n0 + warp, t = p.reverse ? len - 1 - n : n;
+        const bool live = n < len;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int r = lane + 32 * j;
+            fq[j] = live && r < p.dk ? to_f32(q[(size_t)t * p.q_tok + r]) : 0.f;
+            fk[j] = live && r < p.dk ? to_f32(k[(size_t)t * p.k_tok + r]) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < JV; ++j) {
+            const int c = lane + 32 * j;
+            fv[j] = live && c < ncol ? to_f32(v[(size_t)t * p.v_tok + c]) : 0.f;
+        }
+    };
+    fetch(0);
     float ghi, glo;
     la_decay_pair(la_clamp_decay(p.log_decay[h]), 1.f, ghi, glo);
 
     for (int n0 = 0; n0 < len; n0 += kRecTok) {
         const int nt = min(kRecTok, len - n0);
-        // stage the group's rows (scan order)
-        for (int i = tid; i < nt * p.dk; i += kRecThreads) {
-            const int tt = i / p.dk, r = i - tt * p.dk;
-            const int t = p.reverse ? len - 1 - (n0 + tt) : n0 + tt;
-            sq[tt][r] = to_f32(q[(size_t)t * p.q_tok + r]);
-            sk[tt][r] = to_f32(k[(size_t)t * p.k_tok + r]) * p.s_in;
-        }
-        for (int i = tid; i < nt * ncol; i += kRecThreads) {
-            const int tt = i / ncol, c = i - tt * ncol;
-            const int t = p.reverse ? len - 1 - (n0 + tt) : n0 + tt;
-            sv[tt][c] = to_f32(v[(size_t)t * p.v_tok + c]);
-        }
-        __syncthreads();
-        if (col_ok) {
-            for (int tt = 0; tt < nt; ++tt) {
-                const float4 vv = *reinterpret_cast<const float4*>(&sv[tt][cq]);
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int m = 0; m < MAXM; ++m) {
-                    const int r = rr + m * rows_par;
-                    if (r < p.dk) {
-                        const float kr = sk[tt][r], qr = sq[tt][r];
-                        float4 a = s[m];
-                        if (SHIFT) {
-                            a = make_float4(fmaf(kr, vv.x, a.x), fmaf(kr, vv.y, a.y), fmaf(kr, vv.z, a.z), fmaf(kr, vv.w, a.w));
-                        } else {
-                            a.x = fmaf(a.x, ghi, fmaf(a.x, glo, kr * vv.x));
-                            a.y = fmaf(a.y, ghi, fmaf(a.y, glo, kr * vv.y));
-                            a.z = fmaf(a.z, ghi, fmaf(a.z, glo, kr * vv.z));
-                            a.w = fmaf(a.w, ghi, fmaf(a.w, glo, kr * vv.w));
-                        }
-                        o.x = fmaf(qr, a.x, o.x);
-                        o.y = fmaf(qr, a.y, o.y);
-                        o.z = fmaf(qr, a.z, o.z);
-                        o.w = fmaf(qr, a.w, o.w);
-                        if (SHIFT) {
-                            a.x = fmaf(a.x, ghi, a.x * glo);
-                            a.y = fmaf(a.y, ghi, a.y * glo);
-                            a.z = fmaf(a.z, ghi, a.z * glo);
-                            a.w = fmaf(a.w, ghi, a.w * glo);
-                        }
-                        s[m] = a;
-                    }
+        for (int j = 0; j < J; ++j) sqk[warp][lane + 32 * j] = make_float2(fq[j], fk[j] * p.s_in);
+#pragma unroll
+        for (int j = 0; j < JV; ++j)
+            if (lane + 32 * j < COLS) sv[warp][lane + 32 * j] = fv[j];
+        __syncthreads();
+        fetch(n0 + kRecTok);
+        for (int tt = 0; tt < nt; ++tt) {
+            const float4 vv = *reinterpret_cast<const float4*>(&sv[tt][cq]);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                if (m * ROWS >= p.dk) break;  // the same for the whole CTA; rows past dk hold zeros throughout
+                const float2 qk = sqk[tt][rr + m * ROWS];
+                float4 a = s[m];
+                if (p.shift) {
+                    a = make_float4(fmaf(qk.y, vv.x, a.x), fmaf(qk.y, vv.y, a.y), fmaf(qk.y, vv.z, a.z), fmaf(qk.y, vv.w, a.w));
+                } else {
+                    a.x = fmaf(a.x, ghi, fmaf(a.x, glo, qk.y * vv.x));
+                    a.y = fmaf(a.y, ghi, fmaf(a.y, glo, qk.y * vv.y));
+                    a.z = fmaf(a.z, ghi, fmaf(a.z, glo, qk.y * vv.z));
+                    a.w = fmaf(a.w, ghi, fmaf(a.w, glo, qk.y * vv.w));
                 }
-                *reinterpret_cast<float4*>(&part[tt][rr * cols + cq]) = o;
+                o.x = fmaf(qk.x, a.x, o.x);
+                o.y = fmaf(qk.x, a.y, o.y);
+                o.z = fmaf(qk.x, a.z, o.z);
+                o.w = fmaf(qk.x, a.w, o.w);
+                if (p.shift) {
+                    a.x = fmaf(a.x, ghi, a.x * glo);
+                    a.y = fmaf(a.y, ghi, a.y * glo);
+                    a.z = fmaf(a.z, ghi, a.z * glo);
+                    a.w = fmaf(a.w, ghi, a.w * glo);
+                }
+                s[m] = a;
+            }
+            // the warp's W rows: each step halves what a lane sums, down to one column a lane
+            if constexpr (W == 1) {
+                *reinterpret_cast<float4*>(&part[tt][warp][cq]) = o;
+            } else {
+                const bool hi = lane & TPR;
+                const float sx = hi ? o.x : o.z, sy = hi ? o.y : o.w;
+                float2 u = hi ? make_float2(o.z, o.w) : make_float2(o.x, o.y);
+                u.x += __shfl_xor_sync(0xffffffffu, sx, TPR);
+                u.y += __shfl_xor_sync(0xffffffffu, sy, TPR);
+                if constexpr (W == 2) {
+                    *reinterpret_cast<float2*>(&part[tt][warp][cq + (hi ? 2 : 0)]) = u;
+                } else {
+                    const bool hi2 = lane & (2 * TPR);
+                    float w = hi2 ? u.y : u.x;
+                    w += __shfl_xor_sync(0xffffffffu, hi2 ? u.x : u.y, 2 * TPR);
+                    if constexpr (W == 8) w += __shfl_xor_sync(0xffffffffu, w, 4 * TPR);
+                    if (W == 4 || lane < 4 * TPR) part[tt][warp][cq + (hi ? 2 : 0) + (hi2 ? 1 : 0)] = w;
+                }
             }
         }
         __syncthreads();
-        for (int i = tid; i < nt * ncol; i += kRecThreads) {
-            const int tt = i / ncol, c = i - tt * ncol;
-            float o = 0.f;
-            for (int g = 0; g < rows_par; ++g) o += part[tt][g * cols + c];
-            const int t = p.reverse ? len - 1 - (n0 + tt) : n0 + tt;
-            la_store(y + (size_t)t * p.y_tok + c, o * p.s_out);
+        for (int i = tid; i < nt * COLS; i += kRecThreads) {
+            const int tt = i / COLS, c = i % COLS;
+            if (c < ncol) {
+                float o = 0.f;
+#pragma unroll
+                for (int g = 0; g < kRecThreads / 32; ++g) o += part[tt][g][c];
+                const int t = p.reverse ? len - 1 - (n0 + tt) : n0 + tt;
+                la_store(p, y0 + (size_t)t * p.y_tok + c, o * p.s_out, T());
+            }
         }
-        // the next group's staging writes sq, sk and sv, last read before the barrier above; `part` is
-        // written again only behind the next group's first barrier
+        // the staging of the next group writes sqk and sv, last read before the barrier above; `part` is written
+        // again only behind the next group's first barrier
     }
     if (tid < ncol)
-        for (int t = len; t < p.seq_len; ++t) la_store(y + (size_t)t * p.y_tok + tid, 0.f);
+        for (int t = len; t < p.seq_len; ++t) la_store(p, y0 + (size_t)t * p.y_tok + tid, 0.f, T());
     if (p.h_last && col_ok) {
 #pragma unroll
-        for (int m = 0; m < MAXM; ++m) {
-            const int r = rr + m * rows_par;
+        for (int m = 0; m < M; ++m) {
+            const int r = rr + m * ROWS;
             if (r < p.dk) {
                 if (!p.h_t) {
                     *reinterpret_cast<float4*>(p.h_last + sbase + (size_t)r * p.dv + c0 + cq) = s[m];
@@ -147,27 +192,111 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(LaPass p, int 
     }
 }
 
-// ------------------------------------------------------------------------------------ host
+// One token of every sequence (no shift, no lengths): a stream over the states.  The layout is the kernel's above; the
+// rows are taken kStepRows at a time, all of their loads in flight at once, and written back as they are updated.
+constexpr int kStepRows = 4;
 
-template <typename T, typename TY, int MAXM>
-inline cudaError_t linattn_rec_launch_m(const LaPass& p, int cols, cudaStream_t stream) {
-    const dim3 grid((unsigned)((long long)p.nseq * p.heads), (unsigned)((p.dv + cols - 1) / cols));
-    if (p.shift) return launch_pdl(linattn_rec_kernel<T, TY, MAXM, true>, grid, dim3(kRecThreads), 0, stream, p, cols);
-    return launch_pdl(linattn_rec_kernel<T, TY, MAXM, false>, grid, dim3(kRecThreads), 0, stream, p, cols);
+template <typename T>
+__global__ void __launch_bounds__(kRecThreads, 4) linattn_step_kernel(const __grid_constant__ LaPass p, int cols) {
+    __shared__ float sq[kRecMaxD], sk[kRecMaxD];
+    __shared__ __align__(16) float part[kRecThreads * 4];  // [row group][cols]
+    const int tid = threadIdx.x;
+    const int tpr = cols >> 2, rows_par = kRecThreads / tpr;
+    const int rr = tid / tpr, cq = (tid - rr * tpr) * 4;
+    const int c0 = blockIdx.y * cols, ncol = min(cols, p.dv - c0);
+    const bool col_ok = tid < tpr * rows_par && cq < ncol;
+    pdl_trigger();
+    pdl_wait();
+
+    const long long item = blockIdx.x;
+    const int seq = (int)(item / p.heads), h = (int)(item - (long long)seq * p.heads);
+    const float* in = p.h0 + (size_t)item * p.dk * p.dv + c0 + cq;
+    float* out = p.h_last + (size_t)item * p.dk * p.dv + c0 + cq;
+    float4 s[kStepRows];
+    auto load = [&](int m0) {
+#pragma unroll
+        for (int m = 0; m < kStepRows; ++m) {
+            const int r = rr + (m0 + m) * rows_par;
+            if (col_ok && r < p.dk) s[m] = *reinterpret_cast<const float4*>(in + (size_t)r * p.dv);
+        }
+    };
+    load(0);
+    const T* q = static_cast<const T*>(p.q) + (size_t)seq * p.q_tok + (size_t)(h / p.q_div) * p.dk;
+    const T* k = static_cast<const T*>(p.k) + (size_t)seq * p.k_tok + (size_t)(h / p.k_div) * p.dk;
+    const T* v = static_cast<const T*>(p.v) + (size_t)seq * p.v_tok + (size_t)(h / p.v_div) * p.dv + c0 + cq;
+    for (int i = tid; i < p.dk; i += kRecThreads) {
+        sq[i] = to_f32(q[i]);
+        sk[i] = to_f32(k[i]) * p.s_in;
+    }
+    float4 vv = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col_ok) vv = make_float4(to_f32(v[0]), to_f32(v[1]), to_f32(v[2]), to_f32(v[3]));
+    // gamma in two parts, as la_decay_pair, while the loads are on their way
+    const double e = exp((double)la_clamp_decay(p.log_decay[h]));
+    const float ghi = (float)e, glo = (float)(e - (double)ghi);
+    __syncthreads();
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int m0 = 0; rr + m0 * rows_par < p.dk; m0 += kStepRows) {
+        if (m0 > 0) load(m0);
+#pragma unroll
+        for (int m = 0; m < kStepRows; ++m) {
+            const int r = rr + (m0 + m) * rows_par;
+            if (col_ok && r < p.dk) {
+                const float kr = sk[r], qr = sq[r];
+                float4 a = s[m];
+                a.x = fmaf(a.x, ghi, fmaf(a.x, glo, kr * vv.x));
+                a.y = fmaf(a.y, ghi, fmaf(a.y, glo, kr * vv.y));
+                a.z = fmaf(a.z, ghi, fmaf(a.z, glo, kr * vv.z));
+                a.w = fmaf(a.w, ghi, fmaf(a.w, glo, kr * vv.w));
+                *reinterpret_cast<float4*>(out + (size_t)r * p.dv) = a;
+                o.x = fmaf(qr, a.x, o.x);
+                o.y = fmaf(qr, a.y, o.y);
+                o.z = fmaf(qr, a.z, o.z);
+                o.w = fmaf(qr, a.w, o.w);
+            }
+        }
+    }
+    if (col_ok) *reinterpret_cast<float4*>(&part[rr * cols + cq]) = o;
+    __syncthreads();
+    if (tid < ncol) {
+        float y = 0.f;
+        for (int g = 0; g < rows_par; ++g) y += part[g * cols + tid];
+        static_cast<T*>(p.y)[(size_t)seq * p.y_tok + (size_t)h * p.dv + c0 + tid] = from_f32<T>(y * p.s_out);
+    }
 }
 
-// Columns per CTA: all of them when the (sequence, head) pairs fill the GPU, else half or a quarter, so
-// that a few heads still spread over the SMs.
-template <typename T, typename TY>
-inline cudaError_t linattn_rec_launch(const LaPass& p, int nsm, cudaStream_t stream) {
+// ------------------------------------------------------------------------------------ host
+
+// `n` passes over the same sequences and heads in one launch.  Columns per CTA: as many as the widest pass has when the
+// (sequence, head) pairs fill the GPU, fewer (down to 16) when few heads have to spread over the SMs.
+template <typename T>
+inline cudaError_t linattn_rec_launch(const LaPass* p, int n, int nsm, cudaStream_t stream) {
+    LaPasses all;
+    std::memset(&all, 0, sizeof(all));
+    int dv = 0;
+    for (int i = 0; i < n; ++i) {
+        all.p[i] = p[i];
+        dv = std::max(dv, p[i].dv);
+    }
+    const long long items = (long long)p[0].nseq * p[0].heads;
+    int tpr = 32;
+    while (tpr > 4 && (4 * tpr >= 2 * dv || items * n * ((dv + 4 * tpr - 1) / (4 * tpr)) < 2LL * nsm)) tpr >>= 1;
+    const dim3 grid((unsigned)items, (unsigned)((dv + 4 * tpr - 1) / (4 * tpr)), (unsigned)n);
+    switch (tpr) {
+        case 32: return launch_pdl(linattn_rec_kernel<T, 32>, grid, dim3(kRecThreads), 0, stream, all);
+        case 16: return launch_pdl(linattn_rec_kernel<T, 16>, grid, dim3(kRecThreads), 0, stream, all);
+        case 8: return launch_pdl(linattn_rec_kernel<T, 8>, grid, dim3(kRecThreads), 0, stream, all);
+        default: return launch_pdl(linattn_rec_kernel<T, 4>, grid, dim3(kRecThreads), 0, stream, all);
+    }
+}
+
+// The serving step: h0 and h_last given, one token.
+template <typename T>
+inline cudaError_t linattn_step_launch(const LaPass& p, int nsm, cudaStream_t stream) {
     const long long items = (long long)p.nseq * p.heads;
     int cols = p.dv;
     while (cols > 32 && items * ((p.dv + cols - 1) / cols) < 2LL * nsm) cols = (cols / 2 + 3) & ~3;
-    const int rows_par = kRecThreads / (cols / 4);
-    const int m = (p.dk + rows_par - 1) / rows_par;
-    if (m <= 4) return linattn_rec_launch_m<T, TY, 4>(p, cols, stream);
-    if (m <= 8) return linattn_rec_launch_m<T, TY, 8>(p, cols, stream);
-    return linattn_rec_launch_m<T, TY, 16>(p, cols, stream);
+    const dim3 grid((unsigned)items, (unsigned)((p.dv + cols - 1) / cols));
+    return launch_pdl(linattn_step_kernel<T>, grid, dim3(kRecThreads), 0, stream, p, cols);
 }
 
 // h_last = h0 (or zero) where there is no token at all.

@@ -178,13 +178,18 @@ struct LaItem {
     float g;
 };
 
+// This CTA's share of the work: [begin, end).
+__device__ __forceinline__ int la_share(int nwork, unsigned i) { return (int)((unsigned long long)nwork * i / gridDim.x); }
+
 template <bool Y>
 __device__ __forceinline__ LaItem la_item(const TcLaunch& L, int work) {
     const LaPass& p = L.p;
     const int runs = Y ? L.nseg : L.nseg - 1;  // the last segment's state is nobody's start
     LaItem it;
-    it.h = work % p.heads;
-    const int rest = work / p.heads, seg = rest % runs;
+    // heads slowest: a CTA's items mostly share their head, and with it the decay's tables
+    const int per_head = p.nseq * runs;
+    it.h = work / per_head;
+    const int rest = work - it.h * per_head, seg = rest % runs;
     it.seq = rest / runs;
     it.len = la_len(p, it.seq);
     it.nch = (it.len + kLaTok - 1) / kLaTok;
@@ -369,6 +374,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
     pdl_trigger();
     pdl_wait();
 
+    const int work0 = la_share(L.nwork, blockIdx.x), work1 = la_share(L.nwork, blockIdx.x + 1);
     bool ok = true;
     uint32_t issued = 0;  // chunks whose loads were issued (producer)
 
@@ -376,8 +382,15 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         // ------------------------------------------------------------------ producer
         const uint32_t tx = (uint32_t)(Cfg::StageBytes / kLaBlock) * (uint32_t)L.box_rows * 128u;
         uint32_t pos = 0;
-        for (int work = blockIdx.x; work < L.nwork && ok; work += gridDim.x) {
+        for (int work = work0; work < work1 && ok; ++work) {
             const LaItem it = la_item<Y>(L, work);
+            if (work + 1 < work1 && elect_one()) {
+                // the next item's initial state into L2: its load stands at the head of that item's chain
+                const float* in = la_item<Y>(L, work + 1).in;
+                if (in)
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(in), "r"(p.dk * p.dv * 4) : "memory");
+            }
+            __syncwarp();
             const int hq = it.h / p.q_div, hk = it.h / p.k_div, hv = it.h / p.v_div;
             for (int c = it.a; c < it.b; ++c, ++pos) {
                 const int st = pos % NST;
@@ -407,7 +420,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         const uint32_t dv = la_mn_desc(smem_addr(smem + Cfg::QBytes + Cfg::KBytes));
         const uint32_t dkt = la_mn_desc(smem_addr(kt)), dp = la_k_desc(smem_addr(pbuf));
         uint32_t total = 0;
-        for (int work = blockIdx.x; work < L.nwork; work += gridDim.x) {
+        for (int work = work0; work < work1; ++work) {
             const LaItem it = la_item<Y>(L, work);
             total += (uint32_t)(it.b - it.a);
         }
@@ -429,7 +442,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
             return true;
         };
         uint32_t pos = 0, nqs = 0, nqk = 0;
-        for (int work = blockIdx.x; work < L.nwork && ok; work += gridDim.x) {
+        for (int work = work0; work < work1 && ok; ++work) {
             const LaItem it = la_item<Y>(L, work);
             for (int c = it.a; c < it.b && ok; ++c, ++pos) {
                 const bool has = it.in || c > it.a, need = c < it.b - 1 || it.out;
@@ -506,8 +519,12 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         const bool live = row < p.dv;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
         float2 S[H / 2];
+        // of the head and chunk length at hand: the chunk's decay, and the weights of the two tokens whose keys this
+        // thread scales
+        float dhi = 0.f, dlo = 0.f, kw[2] = {0.f, 0.f};
+        int head = -1, kw_n = -1;
         uint32_t pos = 0, nkv = 0, nqs = 0;
-        for (int work = blockIdx.x; work < L.nwork && ok; work += gridDim.x) {
+        for (int work = work0; work < work1 && ok; ++work) {
             const LaItem it = la_item<Y>(L, work);
 #pragma unroll
             for (int i = 0; i < H / 2; ++i) S[i] = make_float2(0.f, 0.f);
@@ -528,10 +545,10 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                         if (k0 + i < p.dk) S[i / 2] = make_float2(a[(size_t)i * p.dv], a[(size_t)(i + 1) * p.dv]);
                 }
             }
-            // of a full chunk: its decay, and the weights of the two tokens whose keys this thread scales
-            float ghi, glo, kw[2], dhi, dlo;
-            int kw_n = -1;
-            if (it.b - it.a > 1 || it.out) la_decay_pair(it.g, (float)kLaTok, ghi, glo);
+            if (it.h != head) {
+                head = it.h;
+                kw_n = -1;
+            }
             for (int c = it.a; c < it.b; ++c, ++pos) {
                 const bool has = it.in || c > it.a, need = c < it.b - 1 || it.out;
                 int row0, n;
@@ -542,8 +559,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     unsigned char* s = smem + st * Cfg::StageBytes;
                     if (n != kw_n) {
                         kw_n = n;
-                        dhi = ghi, dlo = glo;
-                        if (n != kLaTok) la_decay_pair(it.g, (float)n, dhi, dlo);
+                        la_decay_pair(it.g, (float)n, dhi, dlo);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int j = (tid >> 3) + 32 * e;
@@ -646,11 +662,15 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         const uint32_t lane_off = (uint32_t)c0 << 16;
         const bool used = c0 < p.dv;                      // warp-uniform
         const int fr = lane >> 2, fc = (lane & 3) * 2;    // this thread's row and column of an 8 x 8 fragment
+        float2 fac[8];  // s_out gamma^(position + 1 - shift) of tokens 8 k + fc, 8 k + fc + 1, for the head and chunk length
+        int head = -1, fac_n = -1;
         uint32_t pos = 0;
-        for (int work = blockIdx.x; work < L.nwork && ok; work += gridDim.x) {
+        for (int work = work0; work < work1 && ok; ++work) {
             const LaItem it = la_item<Y>(L, work);
-            float2 fac[8];  // s_out gamma^(position + 1 - shift) of tokens 8 k + fc, 8 k + fc + 1
-            int fac_n = -1;
+            if (it.h != head) {
+                head = it.h;
+                fac_n = -1;
+            }
             for (int c = it.a; c < it.b; ++c, ++pos) {
                 const bool has = it.in || c > it.a;
                 const int st = pos % NST;
@@ -775,12 +795,14 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                 *reinterpret_cast<uint4*>(prow + part * Cfg::PPart + q * 16) = make_uint4(0, 0, 0, 0);
         __syncwarp();
         const float s = p.s_in * p.s_out;
+        // weights of this row, for the head at hand: on the diagonal block, and on the full one (its columns are farther)
+        float2 wd[16], wo[16];
+        int head = -1;
         uint32_t pos = 0;
-        for (int work = blockIdx.x; work < L.nwork && ok; work += gridDim.x) {
+        for (int work = work0; work < work1 && ok; ++work) {
             const LaItem it = la_item<Y>(L, work);
-            // weights of this row: on the diagonal block, and on the full one (its columns are farther)
-            float2 wd[16], wo[16];
-            if (it.b > it.a) {
+            if (it.b > it.a && it.h != head) {
+                head = it.h;
                 __syncwarp();
                 wtab[lane] = s * la_decay_pow(it.g, (float)lane);
                 wtab[lane + 32] = s * la_decay_pow(it.g, (float)(lane + 32));

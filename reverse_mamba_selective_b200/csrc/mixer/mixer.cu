@@ -108,12 +108,16 @@ size_t pass_bytes(const r2l_linattn_args* a) {
     return align256(la_segment_bytes(a->batch * nblk, a->n_heads, len, a->d_k, a->d_v, sm_count()));
 }
 
-bool run_pass(const LaPass& p, r2l_dtype dtype, void* seg, cudaStream_t stream) {
+// `n` passes over the same sequences and heads; seg: pass_bytes bytes, used by one after another.
+bool run_passes(const LaPass* p, int n, r2l_dtype dtype, void* seg, cudaStream_t stream) {
     const int nsm = sm_count();
-    if (on_tensor_cores(dtype, p.seq_len)) return linattn_tc_launch(p, static_cast<float*>(seg), nsm, stream);
-    const cudaError_t e = dtype == R2L_F32 ? linattn_rec_launch<float, float>(p, nsm, stream)
-                          : p.y_f32        ? linattn_rec_launch<__nv_bfloat16, float>(p, nsm, stream)
-                                           : linattn_rec_launch<__nv_bfloat16, __nv_bfloat16>(p, nsm, stream);
+    if (on_tensor_cores(dtype, p->seq_len)) {
+        for (int i = 0; i < n; ++i)
+            if (!linattn_tc_launch(p[i], static_cast<float*>(seg), nsm, stream)) return false;
+        return true;
+    }
+    const cudaError_t e = dtype == R2L_F32 ? linattn_rec_launch<float>(p, n, nsm, stream)
+                                           : linattn_rec_launch<__nv_bfloat16>(p, n, nsm, stream);
     return cuda_ok(e, "linear attention kernel launch");
 }
 
@@ -126,14 +130,20 @@ r2l_status copy_state(const float* h0, float* h_last, size_t n, cudaStream_t str
                : R2L_ERR_CUDA;
 }
 
-// Workspace of the backward call: per-head fp32 gradients of shared heads (each of dq, dk, dv that needs them
-// uses the same space in turn).
-size_t bwd_part_bytes(const r2l_linattn_args* a) {
+// Workspace of the backward call: per-head fp32 gradients of those of q, k, v whose heads are shared.
+struct BwdParts {
+    size_t off[3], total;
+};
+BwdParts bwd_parts(const r2l_linattn_args* a) {
     const size_t rows = (size_t)a->batch * a->seqlen * a->n_heads;
-    size_t need = 0;
-    if (a->q_heads != a->n_heads || a->k_heads != a->n_heads) need = std::max(need, rows * a->d_k * sizeof(float));
-    if (a->v_heads != a->n_heads) need = std::max(need, rows * a->d_v * sizeof(float));
-    return align256(need);
+    const int groups[3] = {a->q_heads, a->k_heads, a->v_heads}, d[3] = {a->d_k, a->d_k, a->d_v};
+    BwdParts w;
+    w.total = 0;
+    for (int i = 0; i < 3; ++i) {
+        w.off[i] = w.total;
+        if (groups[i] != a->n_heads) w.total += align256(rows * d[i] * sizeof(float));
+    }
+    return w;
 }
 
 bool bad_workspace(const void* ws, size_t have, size_t need) { return need > 0 && (!ws || !aligned256(ws) || have < need); }
@@ -160,7 +170,8 @@ r2l_status r2l_linattn(const r2l_linattn_args* a, const float* h0, float* h_last
     if (a->seqlen == 0) return copy_state(h0, h_last, (size_t)a->batch * a->n_heads * a->d_k * a->d_v, stream);
     if (!y || !aligned16(y)) return R2L_ERR_INVALID_ARG;
     if (bad_workspace(workspace, workspace_bytes, r2l_linattn_workspace_size(a))) return R2L_ERR_INVALID_ARG;
-    return run_pass(forward_pass(a, h0, h_last, y), a->dtype, workspace, stream) ? R2L_OK : R2L_ERR_CUDA;
+    const LaPass p = forward_pass(a, h0, h_last, y);
+    return run_passes(&p, 1, a->dtype, workspace, stream) ? R2L_OK : R2L_ERR_CUDA;
 }
 
 r2l_status r2l_linattn_step(const r2l_linattn_args* a, const float* h, float* h_out, void* y, cudaStream_t stream) {
@@ -170,14 +181,14 @@ r2l_status r2l_linattn_step(const r2l_linattn_args* a, const float* h, float* h_
     if (la_empty(a)) return R2L_OK;
     if (!h || !h_out || !y || !aligned16(h) || !aligned16(h_out) || !aligned16(y)) return R2L_ERR_INVALID_ARG;
     const LaPass p = forward_pass(a, h, h_out, y);
-    const cudaError_t e = a->dtype == R2L_F32 ? linattn_rec_launch<float, float>(p, sm_count(), stream)
-                                              : linattn_rec_launch<__nv_bfloat16, __nv_bfloat16>(p, sm_count(), stream);
+    const cudaError_t e = a->dtype == R2L_F32 ? linattn_step_launch<float>(p, sm_count(), stream)
+                                              : linattn_step_launch<__nv_bfloat16>(p, sm_count(), stream);
     return cuda_ok(e, "linear attention step launch") ? R2L_OK : R2L_ERR_CUDA;
 }
 
 size_t r2l_linattn_bwd_workspace_size(const r2l_linattn_args* a) {
     if (check_linattn(a) != R2L_OK || la_empty(a) || a->seqlen == 0) return 0;
-    return bwd_part_bytes(a) + pass_bytes(a);
+    return bwd_parts(a).total + pass_bytes(a);
 }
 
 r2l_status r2l_linattn_bwd(const r2l_linattn_args* a, const void* dy, const float* h0, const float* dh_last, void* dq,
@@ -194,57 +205,55 @@ r2l_status r2l_linattn_bwd(const r2l_linattn_args* a, const void* dy, const floa
 
     const LaPass f = forward_pass(a, h0, nullptr, nullptr);
     const long long rows = (long long)a->batch * a->seqlen, dy_tok = (long long)a->n_heads * a->d_v;
-    void* seg = static_cast<unsigned char*>(workspace) + bwd_part_bytes(a);
-    // one pass into the gradient itself, or (shared heads) into the workspace and summed from there
-    auto gradient = [&](LaPass p, void* out, int groups) -> bool {
-        const int div = a->n_heads / groups;
-        p.y_tok = (long long)a->n_heads * p.dv;
-        p.y = div > 1 ? workspace : out;
-        p.y_f32 = div > 1;
-        if (!run_pass(p, a->dtype, seg, stream)) return false;
-        if (div == 1) return true;
-        const size_t n = (size_t)rows * groups * p.dv;
-        const unsigned blocks = (unsigned)std::min<size_t>((n + 255) / 256, 148 * 16);
-        const float* part = static_cast<const float*>(workspace);
-        const cudaError_t e =
-            a->dtype == R2L_BF16
-                ? launch_pdl(linattn_sum_heads_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, stream, part,
-                             static_cast<__nv_bfloat16*>(out), n, groups, div, p.dv)
-                : launch_pdl(linattn_sum_heads_kernel<float>, dim3(blocks), dim3(256), 0, stream, part,
-                             static_cast<float*>(out), n, groups, div, p.dv);
-        return cuda_ok(e, "linear attention head sum launch");
-    };
+    const BwdParts parts = bwd_parts(a);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    LaPass p[3] = {f, f, f};
     // dq = (dy, v, k) in scan order from h0 transposed
-    LaPass p = f;
-    p.q = dy, p.q_tok = dy_tok, p.q_div = 1;
-    p.k = f.v, p.k_tok = f.v_tok, p.k_div = f.v_div;
-    p.v = f.k, p.v_tok = f.k_tok, p.v_div = f.k_div;
-    p.dk = a->d_v, p.dv = a->d_k;
-    p.h_t = 1;
-    if (!gradient(p, dq, a->q_heads)) return R2L_ERR_CUDA;
+    p[0].q = dy, p[0].q_tok = dy_tok, p[0].q_div = 1;
+    p[0].k = f.v, p[0].k_tok = f.v_tok, p[0].k_div = f.v_div;
+    p[0].v = f.k, p[0].v_tok = f.k_tok, p[0].v_div = f.k_div;
+    p[0].dk = a->d_v, p[0].dv = a->d_k;
+    p[0].h_t = 1;
     // dk = (v, dy, q) against the scan order, the adjoint state transposed
-    p = f;
-    p.q = f.v, p.q_tok = f.v_tok, p.q_div = f.v_div;
-    p.k = dy, p.k_tok = dy_tok, p.k_div = 1;
-    p.v = f.q, p.v_tok = f.q_tok, p.v_div = f.q_div;
-    p.dk = a->d_v, p.dv = a->d_k;
-    p.h_t = 1;
-    p.reverse = !f.reverse;
-    p.shift = 1;
-    p.s_in = a->scale, p.s_out = 1.f;
-    p.h0 = dh_last;
-    if (!gradient(p, dk, a->k_heads)) return R2L_ERR_CUDA;
+    p[1].q = f.v, p[1].q_tok = f.v_tok, p[1].q_div = f.v_div;
+    p[1].k = dy, p[1].k_tok = dy_tok, p[1].k_div = 1;
+    p[1].v = f.q, p[1].v_tok = f.q_tok, p[1].v_div = f.q_div;
+    p[1].dk = a->d_v, p[1].dv = a->d_k;
+    p[1].h_t = 1;
     // dv = (k, q, dy) against the scan order; its final state is dh0
-    p = f;
-    p.q = f.k, p.q_tok = f.k_tok, p.q_div = f.k_div;
-    p.k = f.q, p.k_tok = f.q_tok, p.k_div = f.q_div;
-    p.v = dy, p.v_tok = dy_tok, p.v_div = 1;
-    p.reverse = !f.reverse;
-    p.shift = 1;
-    p.s_in = a->scale, p.s_out = 1.f;
-    p.h0 = dh_last;
-    p.h_last = dh0;
-    if (!gradient(p, dv, a->v_heads)) return R2L_ERR_CUDA;
+    p[2].q = f.k, p[2].q_tok = f.k_tok, p[2].q_div = f.k_div;
+    p[2].k = f.q, p[2].k_tok = f.q_tok, p[2].k_div = f.q_div;
+    p[2].v = dy, p[2].v_tok = dy_tok, p[2].v_div = 1;
+    for (int i = 1; i < 3; ++i) {
+        p[i].reverse = !f.reverse;
+        p[i].shift = 1;
+        p[i].s_in = a->scale, p[i].s_out = 1.f;
+        p[i].h0 = dh_last;
+    }
+    p[2].h_last = dh0;
+    // each into the gradient itself, or (shared heads) per head into the workspace and summed from there
+    void* outs[3] = {dq, dk, dv};
+    const int groups[3] = {a->q_heads, a->k_heads, a->v_heads};
+    for (int i = 0; i < 3; ++i) {
+        const bool shared = groups[i] != a->n_heads;
+        p[i].y = shared ? static_cast<void*>(ws + parts.off[i]) : outs[i];
+        p[i].y_f32 = shared;
+        p[i].y_tok = (long long)a->n_heads * p[i].dv;
+    }
+    if (!run_passes(p, 3, a->dtype, ws + parts.total, stream)) return R2L_ERR_CUDA;
+    for (int i = 0; i < 3; ++i) {
+        if (!p[i].y_f32) continue;
+        const int div = a->n_heads / groups[i], d = p[i].dv;
+        const size_t n = (size_t)rows * groups[i] * d;
+        const unsigned blocks = (unsigned)std::min<size_t>((n + 255) / 256, 148 * 16);
+        const float* part = static_cast<const float*>(p[i].y);
+        const cudaError_t e = a->dtype == R2L_BF16
+                                  ? launch_pdl(linattn_sum_heads_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, stream, part,
+                                               static_cast<__nv_bfloat16*>(outs[i]), n, groups[i], div, d)
+                                  : launch_pdl(linattn_sum_heads_kernel<float>, dim3(blocks), dim3(256), 0, stream, part,
+                                               static_cast<float*>(outs[i]), n, groups[i], div, d);
+        if (!cuda_ok(e, "linear attention head sum launch")) return R2L_ERR_CUDA;
+    }
     return R2L_OK;
 }
 
@@ -300,8 +309,9 @@ RopeParams rope_params(const r2l_qk_norm_rope_args* a) {
     return p;
 }
 
+// For the narrowest groups, which need the most CTAs: the alignment of the outputs, not known here, may choose others.
 size_t rope_part_bytes(const r2l_qk_norm_rope_args* a) {
-    return align256((size_t)2 * rope_bwd_ctas(a->tokens) * a->head_dim * sizeof(float));
+    return align256((size_t)2 * rope_bwd_ctas(a->tokens, 32) * a->head_dim * sizeof(float));
 }
 
 }  // namespace
@@ -325,11 +335,10 @@ r2l_status r2l_qk_norm_rope(const r2l_qk_norm_rope_args* a, void* q_out, long lo
         p.out[w] = outs[w];
         p.out_tok[w] = strides[w] ? strides[w] : dense;
     }
-    // few tokens: a CTA each (latency); many: four, which share the set-up
-    p.tok_step = a->tokens <= 4 * sm_count() ? 1 : kRopeTok;
-    const dim3 grid((unsigned)((a->tokens + p.tok_step - 1) / p.tok_step));
-    const cudaError_t e = a->dtype == R2L_BF16 ? rope_launch<false, __nv_bfloat16>(p, grid, stream)
-                                               : rope_launch<false, float>(p, grid, stream);
+    const int heads = a->q_heads + a->k_heads, es = esize(a->dtype);
+    p.split = rope_split(a->tokens, heads, rope_lanes(p, es, false), sm_count());
+    const cudaError_t e = a->dtype == R2L_BF16 ? rope_launch<false, __nv_bfloat16>(p, 0, stream)
+                                               : rope_launch<false, float>(p, 0, stream);
     return cuda_ok(e, "norm and rotation kernel launch") ? R2L_OK : R2L_ERR_CUDA;
 }
 
@@ -362,11 +371,9 @@ r2l_status r2l_qk_norm_rope_bwd(const r2l_qk_norm_rope_args* a, const void* dq_o
         }
         if (want_w && bad_workspace(workspace, workspace_bytes, rope_part_bytes(a))) return R2L_ERR_INVALID_ARG;
         p.part = want_w ? static_cast<float*>(workspace) : nullptr;
-        p.tok_step = kRopeTok;
-        n = rope_bwd_ctas(a->tokens);
-        const dim3 grid((unsigned)n, 2);
-        const cudaError_t e = a->dtype == R2L_BF16 ? rope_launch<true, __nv_bfloat16>(p, grid, stream)
-                                                   : rope_launch<true, float>(p, grid, stream);
+        n = rope_bwd_ctas(a->tokens, rope_lanes(p, esize(a->dtype), true));
+        const cudaError_t e = a->dtype == R2L_BF16 ? rope_launch<true, __nv_bfloat16>(p, n, stream)
+                                                   : rope_launch<true, float>(p, n, stream);
         if (!cuda_ok(e, "norm and rotation gradient launch")) return R2L_ERR_CUDA;
     }
     if (!want_w) return R2L_OK;

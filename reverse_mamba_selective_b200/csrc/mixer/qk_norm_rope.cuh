@@ -1,20 +1,26 @@
 // qk_norm_rope.cuh -- per-head RMS norm of queries and keys with the rotary position embedding, and its
 // gradients.
 //
-// Bound by memory: every head is read once and written once (16-byte pieces).  A group of G lanes owns a
-// head; lane s holds the two pieces that rotate together (channels s V .. and rot / 2 + s V ..), so the
-// rotation needs no exchange and the norm one shuffle tree over the group.  The angles of a token are
-// shared by all its heads: a CTA forms them once for its tokens, in fp64 up to the fraction of a turn
-// (position 100000 x frequency 1 leaves fp32 half a degree), while the first heads are on their way.
+// Bound by memory: every head is read once and written once (16-byte pieces).  A group of G lanes owns a token
+// (or, for few tokens, a share of its heads) and walks over its heads.  Lane s holds the two pieces that rotate together
+// (channels s V .. and rot / 2 + s V ..), the same ones in every head: the rotation needs no exchange, the norm one
+// shuffle tree, and the token's angles and the weights stay in registers.  (Angles and weights in shared memory, read
+// anew for every head, bound the kernel at 3.9 TB/s by bank conflicts.)  The heads ahead are on their way into a ring of
+// shared memory that every lane has to itself, with no barrier: registers for them left too few bytes in flight
+// (4.1 TB/s).  Angles are formed in fp64 up to the
+// fraction of a turn: position 100000 x frequency 1 leaves fp32 half a degree.
 #pragma once
+
+#include <algorithm>
 
 #include "../common.cuh"
 
 namespace r2l {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTok = 4;       // tokens per CTA step (1 for few tokens)
 constexpr int kRopeMaxDim = 256;
+constexpr int kRopeAhead = 4;     // heads that a group has in flight, forward
+constexpr int kRopeAheadBwd = 2;  // and in the gradients (two operands)
 
 struct RopeParams {
     const void *x[2], *dy[2];   // queries, keys
@@ -25,27 +31,51 @@ struct RopeParams {
     float* part;                // [2][gridDim.x][head_dim] partial weight gradients, or NULL
     const void* positions;
     const float* inv_freq;
-    int tokens, dim, rot, interleaved, pos64, tok_step;
+    int tokens, dim, rot, interleaved, pos64;
+    int split;                  // groups that share a token's heads (forward)
     float eps, inv_dim;
 };
 
-// V neighbouring values at p (16 bytes for V > 1), as fp32.
-template <typename T, int V>
-__device__ __forceinline__ void rope_load(const T* p, float (&v)[V]) {
-    if constexpr (V == 1) {
-        v[0] = to_f32(*p);
-    } else if constexpr (sizeof(T) == 4) {
-        const float4 a = *reinterpret_cast<const float4*>(p);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// A lane's values on their way from memory: N heads ahead, each of P pieces of V neighbouring channels (16 bytes for
+// V > 1).  For V > 1 a ring in shared memory, filled by asynchronous copies; single channels are loaded when they are asked for.
+template <typename T, int V, int N, int P>
+struct RopeRing {
+    uint4* mine;  // [N][P][kRopeThreads], this lane's column
+    __device__ __forceinline__ RopeRing(uint4* ring) : mine(ring + threadIdx.x) {}
+    // src NULL: zeros
+    __device__ __forceinline__ void fetch(int slot, int piece, const T* src, const T* any) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(mine + (slot * P + piece) * kRopeThreads)),
+                     "l"(src ? src : any), "r"(src ? 16 : 0)
+                     : "memory");
+    }
+    __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // until at most N - 1 heads are on their way
+    __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N - 1) : "memory"); }
+    __device__ __forceinline__ void get(int slot, int piece, const T*, float (&f)[V]) {
+        const uint4 v = *(mine + (slot * P + piece) * kRopeThreads);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            if constexpr (sizeof(T) == 4) {
+                f[i] = __uint_as_float(w[i]);
+            } else {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
         }
     }
+};
+template <typename T, int N, int P>
+struct RopeRing<T, 1, N, P> {
+    __device__ __forceinline__ RopeRing(uint4*) {}
+    __device__ __forceinline__ void fetch(int, int, const T*, const T*) {}
+    __device__ __forceinline__ void commit() {}
+    __device__ __forceinline__ void wait() {}
+    __device__ __forceinline__ void get(int, int, const T* src, float (&f)[1]) { f[0] = src ? to_f32(*src) : 0.f; }
+};
+template <int V>
+constexpr int rope_ring_bytes(int n, int p) {
+    return V > 1 ? n * p * kRopeThreads * 16 : 0;
 }
 
 template <typename T, int V>
@@ -80,28 +110,46 @@ __device__ __forceinline__ void rope_slot(int s, int dim, int rot, bool inter, i
     if (b >= np) b = -1;
 }
 
-// Rotates the slot's channels; sign -1 takes the rotation back.  cs: (cos, sin) of the token's pairs.
+// The slot's angles: (cos, sin) for the pair i of its channels, (1, 0) where it does not rotate.
+template <int V>
+__device__ __forceinline__ void rope_angles(const RopeParams& p, int token, int a, int b, float2 (&cs)[V]) {
+    const bool inter = p.interleaved != 0;
+    const double pos = p.rot == 0 ? 0.0
+                       : p.pos64  ? (double)static_cast<const long long*>(p.positions)[token]
+                                  : (double)static_cast<const int*>(p.positions)[token];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        int f;  // the pair's frequency
+        if (!inter)
+            f = a < p.rot / 2 / V ? a * V + i : -1;
+        else if constexpr (V == 1)
+            f = a < p.rot ? a >> 1 : -1;
+        else if (i < V / 2)
+            f = a * V < p.rot ? a * V / 2 + i : -1;
+        else
+            f = b * V < p.rot ? b * V / 2 + i - V / 2 : -1;
+        cs[i] = make_float2(1.f, 0.f);
+        if (a >= 0 && f >= 0) {
+            const double turns = pos * (double)__ldg(p.inv_freq + f) * 0.15915494309189535;  // 1 / (2 pi)
+            sincospif((float)(2.0 * (turns - rint(turns))), &cs[i].y, &cs[i].x);
+        }
+    }
+}
+
+// Rotates the slot's channels; sign -1 takes the rotation back.
 template <int V>
 __device__ __forceinline__ void rope_rotate(float (&xa)[V], float (&xb)[V], int a, int b, int rot, bool inter, float sign,
-                                            const float2* cs) {
-    if (!inter) {
-        if (a >= 0 && a < rot / 2 / V) {
+                                            const float2 (&cs)[V]) {
+    if (!inter || V == 1) {
+        if (a >= 0 && (inter ? a < rot : a < rot / 2 / V)) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float2 t = cs[a * V + i];
-                const float sn = sign * t.y, u = xa[i], w = xb[i];
-                xa[i] = u * t.x - w * sn;
-                xb[i] = w * t.x + u * sn;
+                const float sn = sign * cs[i].y, u = xa[i], w = xb[i];
+                xa[i] = u * cs[i].x - w * sn;
+                xb[i] = w * cs[i].x + u * sn;
             }
         }
-    } else if constexpr (V == 1) {
-        if (a >= 0 && a < rot) {
-            const float2 t = cs[a >> 1];
-            const float sn = sign * t.y, u = xa[0], w = xb[0];
-            xa[0] = u * t.x - w * sn;
-            xb[0] = w * t.x + u * sn;
-        }
-    } else {
+    } else if constexpr (V > 1) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float(&x)[V] = half ? xb : xa;
@@ -109,7 +157,7 @@ __device__ __forceinline__ void rope_rotate(float (&xa)[V], float (&xb)[V], int 
             if (piece >= 0 && piece * V < rot) {
 #pragma unroll
                 for (int i = 0; i < V; i += 2) {
-                    const float2 t = cs[(piece * V + i) >> 1];
+                    const float2 t = cs[half * (V / 2) + i / 2];
                     const float sn = sign * t.y, u = x[i], w = x[i + 1];
                     x[i] = u * t.x - w * sn;
                     x[i + 1] = w * t.x + u * sn;
@@ -119,39 +167,20 @@ __device__ __forceinline__ void rope_rotate(float (&xa)[V], float (&xb)[V], int 
     }
 }
 
-// (cos, sin) of the angles of tokens t0 .. t0 + nt - 1 into cs[token][rot / 2].
-__device__ __forceinline__ void rope_angles(const RopeParams& p, int t0, int nt, float2* cs) {
-    const int half = p.rot >> 1;
-    for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
-        const int tt = i / half, f = i - tt * half;
-        const double pos = p.pos64 ? (double)static_cast<const long long*>(p.positions)[t0 + tt]
-                                   : (double)static_cast<const int*>(p.positions)[t0 + tt];
-        const double turns = pos * (double)p.inv_freq[f] * 0.15915494309189535;  // 1 / (2 pi)
-        float sn, cn;
-        sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cn);
-        cs[i] = make_float2(cn, sn);
-    }
-}
-
-// The weights of both operands into shared memory (ones where there are none).
-__device__ __forceinline__ void rope_weights(const RopeParams& p, float (*sw)[kRopeMaxDim]) {
-    for (int i = threadIdx.x; i < 2 * p.dim; i += kRopeThreads) {
-        const int w = i >= p.dim, c = w ? i - p.dim : i;
-        sw[w][c] = p.weight[w] ? p.weight[w][c] : 1.f;
-    }
-}
-
+// The slot's weights of operand w (ones where there are none).
 template <int V>
-__device__ __forceinline__ void rope_weight(const float* sw, float (&v)[V]) {
-    if constexpr (V == 1) {
-        v[0] = *sw;
-    } else {
+__device__ __forceinline__ void rope_weight(const RopeParams& p, int w, int piece, float (&v)[V]) {
+    const float* wt = p.weight[w];
+    if (V >= 4 && piece >= 0 && wt && (reinterpret_cast<uintptr_t>(wt) & 15u) == 0) {
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(sw + i);
+        for (int i = 0; i + 3 < V; i += 4) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(wt + piece * V + i));
             v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
         }
+        return;
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = wt && piece >= 0 ? __ldg(wt + piece * V + i) : 1.f;
 }
 
 template <int G>
@@ -163,13 +192,18 @@ __device__ __forceinline__ float rope_group_sum(float v) {
 
 // G lanes per head, SL slots per lane (SL > 1 only for single channels, V = 1).
 template <typename T, int V, int G, int SL>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
-    __shared__ __align__(16) float2 cs[kRopeTok][kRopeMaxDim / 2];
-    __shared__ __align__(16) float sw[2][kRopeMaxDim];
-    constexpr int kGroups = kRopeThreads / G;
-    const int g = threadIdx.x / G, s0 = threadIdx.x % G;
-    const int t0 = blockIdx.x * p.tok_step, nt = min(p.tok_step, p.tokens - t0);
-    const int ht = p.heads[0] + p.heads[1], nvec = nt * ht;
+__global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int kGroups = kRopeThreads / G, U = kRopeAhead;
+    const int s0 = threadIdx.x % G;
+    const long long item = (long long)blockIdx.x * kGroups + threadIdx.x / G;
+    const int ht = p.heads[0] + p.heads[1], per = (ht + p.split - 1) / p.split;
+    const bool live = item < (long long)p.tokens * p.split;
+    int token = live ? (int)item : 0, h0 = 0;
+    if (p.split > 1 && live) {  // then tokens * split is small
+        token = (int)item / p.split;
+        h0 = ((int)item - token * p.split) * per;
+    }
+    const int hn = live ? min(per, ht - h0) : 0;  // this group's heads: h0 .. h0 + hn - 1 (queries first)
     const bool inter = p.interleaved != 0;
     int pa[SL], pb[SL];
 #pragma unroll
@@ -177,52 +211,65 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
     pdl_trigger();
     pdl_wait();
 
-    float xa[SL][V], xb[SL][V];
-    auto fetch = [&](int vec) {
-        const int tt = vec / ht, hh = vec - tt * ht, w = hh >= p.heads[0];
-        const T* x = static_cast<const T*>(p.x[w]) + (size_t)(t0 + tt) * p.x_tok[w] + (size_t)(w ? hh - p.heads[0] : hh) * p.dim;
-#pragma unroll
-        for (int j = 0; j < SL; ++j) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) xa[j][i] = xb[j][i] = 0.f;
-            if (vec < nvec && pa[j] >= 0) rope_load<T, V>(x + pa[j] * V, xa[j]);
-            if (vec < nvec && pb[j] >= 0) rope_load<T, V>(x + pb[j] * V, xb[j]);
-        }
+    extern __shared__ __align__(16) uint4 rope_ring[];
+    RopeRing<T, V, U, 2> ring(rope_ring);
+    // head i of the group and its slot's pieces (NULL: none)
+    auto source = [&](int i, int piece) -> const T* {
+        const int hh = h0 + i, w = hh >= p.heads[0];
+        if (i >= hn || piece < 0) return nullptr;
+        return static_cast<const T*>(p.x[w]) + (size_t)token * p.x_tok[w] + (size_t)(w ? hh - p.heads[0] : hh) * p.dim + piece * V;
     };
-    fetch(g);
-    rope_weights(p, sw);
-    rope_angles(p, t0, nt, &cs[0][0]);
-    __syncthreads();
-    const int half = p.rot >> 1;
-    for (int v0 = 0; v0 < nvec; v0 += kGroups) {  // uniform over the CTA: the shuffles need whole warps
-        const int vec = v0 + g;
+    const T* any = static_cast<const T*>(p.heads[0] > 0 ? p.x[0] : p.x[1]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        ring.fetch(u, 0, source(u, pa[0]), any);
+        ring.fetch(u, 1, source(u, pb[0]), any);
+        ring.commit();
+    }
+    float2 cs[SL][V];
+#pragma unroll
+    for (int j = 0; j < SL; ++j) rope_angles<V>(p, token, pa[j], pb[j], cs[j]);
+    float wa[SL][V], wb[SL][V];
+    int wcur = -1;
+    // the same count in the whole warp: the shuffles need all lanes
+    int slot = 0;
+    for (int i = 0; i < per; ++i) {
+        const int hh = h0 + i, w = hh >= p.heads[0];
         float ya[SL][V], yb[SL][V], ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < SL; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                ya[j][i] = xa[j][i];
-                yb[j][i] = xb[j][i];
-                ss = fmaf(xa[j][i], xa[j][i], ss);
-                ss = fmaf(xb[j][i], xb[j][i], ss);
-            }
-        if (v0 + kGroups < nvec) fetch(vec + kGroups);
-        const float inv = rsqrtf(fmaf(rope_group_sum<G>(ss), p.inv_dim, p.eps));
-        if (vec >= nvec) continue;
-        const int tt = vec / ht, hh = vec - tt * ht, w = hh >= p.heads[0];
-        T* out = static_cast<T*>(p.out[w]) + (size_t)(t0 + tt) * p.out_tok[w] + (size_t)(w ? hh - p.heads[0] : hh) * p.dim;
-        const float2* tcs = &cs[0][0] + tt * half;
+        ring.wait();
 #pragma unroll
         for (int j = 0; j < SL; ++j) {
-            float wa[V], wb[V];
-            rope_weight<V>(&sw[w][pa[j] >= 0 ? pa[j] * V : 0], wa);
-            rope_weight<V>(&sw[w][pb[j] >= 0 ? pb[j] * V : 0], wb);
+            ring.get(slot, 0, source(i, pa[j]), ya[j]);
+            ring.get(slot, 1, source(i, pb[j]), yb[j]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                ya[j][i] *= inv * wa[i];
-                yb[j][i] *= inv * wb[i];
+            for (int e = 0; e < V; ++e) {
+                ss = fmaf(ya[j][e], ya[j][e], ss);
+                ss = fmaf(yb[j][e], yb[j][e], ss);
             }
-            rope_rotate<V>(ya[j], yb[j], pa[j], pb[j], p.rot, inter, 1.f, tcs);
+        }
+        const float inv = rsqrtf(fmaf(rope_group_sum<G>(ss), p.inv_dim, p.eps));
+        ring.fetch(slot, 0, source(i + U, pa[0]), any);
+        ring.fetch(slot, 1, source(i + U, pb[0]), any);
+        ring.commit();
+        slot = slot + 1 == U ? 0 : slot + 1;
+        if (i >= hn) continue;
+        if (w != wcur) {
+            wcur = w;
+#pragma unroll
+            for (int j = 0; j < SL; ++j) {
+                rope_weight<V>(p, w, pa[j], wa[j]);
+                rope_weight<V>(p, w, pb[j], wb[j]);
+            }
+        }
+        T* out = static_cast<T*>(p.out[w]) + (size_t)token * p.out_tok[w] + (size_t)(w ? hh - p.heads[0] : hh) * p.dim;
+#pragma unroll
+        for (int j = 0; j < SL; ++j) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                ya[j][e] *= inv * wa[j][e];
+                yb[j][e] *= inv * wb[j][e];
+            }
+            rope_rotate<V>(ya[j], yb[j], pa[j], pb[j], p.rot, inter, 1.f, cs[j]);
             if (pa[j] >= 0) rope_store<T, V>(out + pa[j] * V, ya[j]);
             if (pb[j] >= 0) rope_store<T, V>(out + pb[j] * V, yb[j]);
         }
@@ -233,59 +280,60 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
 // from dy: dx = (u w - z mean(u w z)) / rms, dw = sum of u z over tokens and heads.  A lane keeps its channels'
 // share of dw in registers over all its heads; a CTA's groups add theirs in a fixed order at the end.
 template <typename T, int V, int G, int SL>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
-    __shared__ __align__(16) float2 cs[kRopeTok][kRopeMaxDim / 2];
-    __shared__ float red[kRopeThreads / G][kRopeMaxDim < 2 * V * G * SL ? kRopeMaxDim : 2 * V * G * SL];
+__global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const __grid_constant__ RopeParams p) {
     constexpr int kGroups = kRopeThreads / G;
     const int g = threadIdx.x / G, s0 = threadIdx.x % G;
     const int w = blockIdx.y, heads = p.heads[w];
     const bool inter = p.interleaved != 0;
-    const int half = p.rot >> 1;
     int pa[SL], pb[SL];
     float wa[SL][V], wb[SL][V], da[SL][V], db[SL][V];
     pdl_trigger();
     pdl_wait();
-    __shared__ __align__(16) float sw[2][kRopeMaxDim];
-    rope_weights(p, sw);
-    __syncthreads();
 #pragma unroll
     for (int j = 0; j < SL; ++j) {
         rope_slot<V>(s0 + j * G, p.dim, p.rot, inter, pa[j], pb[j]);
-        rope_weight<V>(&sw[w][pa[j] >= 0 ? pa[j] * V : 0], wa[j]);
-        rope_weight<V>(&sw[w][pb[j] >= 0 ? pb[j] * V : 0], wb[j]);
+        rope_weight<V>(p, w, pa[j], wa[j]);
+        rope_weight<V>(p, w, pb[j], wb[j]);
 #pragma unroll
         for (int i = 0; i < V; ++i) da[j][i] = db[j][i] = 0.f;
     }
-    const int steps = (p.tokens + p.tok_step - 1) / p.tok_step;
-    for (int st = blockIdx.x; st < steps && heads > 0; st += gridDim.x) {
-        const int t0 = st * p.tok_step, nt = min(p.tok_step, p.tokens - t0), nvec = nt * heads;
-        __syncthreads();  // the previous step's angles have been read
-        rope_angles(p, t0, nt, &cs[0][0]);
-        __syncthreads();
-        for (int v0 = 0; v0 < nvec; v0 += kGroups) {
-            const int vec = v0 + g;
-            const bool live = vec < nvec;
-            const int tt = live ? vec / heads : 0, hh = live ? vec - tt * heads : 0;
-            const T* x = static_cast<const T*>(p.x[w]) + (size_t)(t0 + tt) * p.x_tok[w] + (size_t)hh * p.dim;
-            const T* dy = static_cast<const T*>(p.dy[w]) + (size_t)(t0 + tt) * p.dy_tok[w] + (size_t)hh * p.dim;
+    extern __shared__ __align__(16) uint4 rope_ring[];
+    constexpr int U = kRopeAheadBwd;
+    RopeRing<T, V, U, 4> ring(rope_ring);
+    // a group walks over whole tokens, kGroups * gridDim.x apart (the same count in the whole CTA)
+    for (long long t0 = (long long)blockIdx.x * kGroups; t0 < p.tokens && heads > 0; t0 += (long long)gridDim.x * kGroups) {
+        const bool live = t0 + g < p.tokens;
+        const int token = live ? (int)(t0 + g) : 0;
+        const T* x = static_cast<const T*>(p.x[w]) + (size_t)token * p.x_tok[w];
+        const T* dy = static_cast<const T*>(p.dy[w]) + (size_t)token * p.dy_tok[w];
+        T* out = static_cast<T*>(p.out[w]) + (size_t)token * p.out_tok[w];
+        auto source = [&](const T* from, int h, int piece) -> const T* {
+            return live && h < heads && piece >= 0 ? from + (size_t)h * p.dim + piece * V : nullptr;
+        };
+        auto fetch = [&](int slot, int h) {
+            ring.fetch(slot, 0, source(x, h, pa[0]), x);
+            ring.fetch(slot, 1, source(x, h, pb[0]), x);
+            ring.fetch(slot, 2, source(dy, h, pa[0]), x);
+            ring.fetch(slot, 3, source(dy, h, pb[0]), x);
+            ring.commit();
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u) fetch(u, u);
+        float2 cs[SL][V];
+#pragma unroll
+        for (int j = 0; j < SL; ++j) rope_angles<V>(p, token, pa[j], pb[j], cs[j]);
+        int slot = 0;
+        for (int h = 0; h < heads; ++h) {
             float xa[SL][V], xb[SL][V], ua[SL][V], ub[SL][V];
             float ss = 0.f, dot = 0.f;
+            ring.wait();
 #pragma unroll
             for (int j = 0; j < SL; ++j) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) xa[j][i] = xb[j][i] = ua[j][i] = ub[j][i] = 0.f;
-                if (live && pa[j] >= 0) {
-                    rope_load<T, V>(x + pa[j] * V, xa[j]);
-                    rope_load<T, V>(dy + pa[j] * V, ua[j]);
-                }
-                if (live && pb[j] >= 0) {
-                    rope_load<T, V>(x + pb[j] * V, xb[j]);
-                    rope_load<T, V>(dy + pb[j] * V, ub[j]);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < SL; ++j) {
-                if (live) rope_rotate<V>(ua[j], ub[j], pa[j], pb[j], p.rot, inter, -1.f, &cs[0][0] + tt * half);
+                ring.get(slot, 0, source(x, h, pa[j]), xa[j]);
+                ring.get(slot, 1, source(x, h, pb[j]), xb[j]);
+                ring.get(slot, 2, source(dy, h, pa[j]), ua[j]);
+                ring.get(slot, 3, source(dy, h, pb[j]), ub[j]);
+                rope_rotate<V>(ua[j], ub[j], pa[j], pb[j], p.rot, inter, -1.f, cs[j]);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     ss = fmaf(xa[j][i], xa[j][i], ss);
@@ -296,8 +344,9 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_bwd_kernel(const __
             }
             const float inv = rsqrtf(fmaf(rope_group_sum<G>(ss), p.inv_dim, p.eps));
             const float m = rope_group_sum<G>(dot) * p.inv_dim * inv * inv;  // mean(u w z) / rms
+            fetch(slot, h + U);
+            slot = slot + 1 == U ? 0 : slot + 1;
             if (!live) continue;
-            T* out = static_cast<T*>(p.out[w]) + (size_t)(t0 + tt) * p.out_tok[w] + (size_t)hh * p.dim;
 #pragma unroll
             for (int j = 0; j < SL; ++j) {
                 float oa[V], ob[V];
@@ -308,24 +357,28 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_bwd_kernel(const __
                     oa[i] = inv * (ua[j][i] * wa[j][i] - xa[j][i] * m);
                     ob[i] = inv * (ub[j][i] * wb[j][i] - xb[j][i] * m);
                 }
-                if (pa[j] >= 0) rope_store<T, V>(out + pa[j] * V, oa);
-                if (pb[j] >= 0) rope_store<T, V>(out + pb[j] * V, ob);
+                if (pa[j] >= 0) rope_store<T, V>(out + (size_t)h * p.dim + pa[j] * V, oa);
+                if (pb[j] >= 0) rope_store<T, V>(out + (size_t)h * p.dim + pb[j] * V, ob);
             }
         }
     }
     if (!p.part) return;
+    // the groups' sums, where the ring was
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(rope_ring);
 #pragma unroll
     for (int j = 0; j < SL; ++j)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (pa[j] >= 0) red[g][pa[j] * V + i] = da[j][i];
-            if (pb[j] >= 0) red[g][pb[j] * V + i] = db[j][i];
+            if (pa[j] >= 0) red[g * p.dim + pa[j] * V + i] = da[j][i];
+            if (pb[j] >= 0) red[g * p.dim + pb[j] * V + i] = db[j][i];
         }
     __syncthreads();
     float* part = p.part + ((size_t)w * gridDim.x + blockIdx.x) * p.dim;
     for (int c = threadIdx.x; c < p.dim; c += kRopeThreads) {
         float s = 0.f;
-        for (int q = 0; q < kGroups; ++q) s += red[q][c];
+        for (int q = 0; q < kGroups; ++q) s += red[q * p.dim + c];
         part[c] = s;
     }
 }
@@ -369,28 +422,53 @@ inline bool rope_wide(const RopeParams& p, int es, bool bwd) {
     return true;
 }
 
+// Groups of a CTA for heads of these parameters: as rope_launch chooses them.
+inline int rope_lanes(const RopeParams& p, int es, bool bwd) {
+    if (!rope_wide(p, es, bwd)) return 32;
+    const int v = 16 / es, slots = (p.dim / v + 1) / 2;
+    return slots <= 4 ? 4 : slots <= 8 ? 8 : slots <= 16 ? 16 : 32;
+}
+
+// Groups per token in the forward kernel: one, which forms the token's angles once, when the tokens alone fill the SMs
+// (768 threads each) twice; for fewer tokens the heads are shared out, up to a group each, and each forms the angles.
+inline int rope_split(int tokens, int heads, int lanes, int nsm) {
+    const long long threads = (long long)tokens * lanes, want = 2LL * nsm * 768;
+    const long long split = threads >= want ? 1 : (want + threads - 1) / threads;
+    return (int)(split < heads ? split : heads);
+}
+
+// CTAs per operand of the gradient kernel: at most two per SM (a wave of both operands), each walking over many
+// tokens, so that the weight gradients leave few partial sums.  Depends on the sizes only.
+inline int rope_bwd_ctas(int tokens, int lanes) {
+    const long long ctas = ((long long)tokens * lanes + kRopeThreads - 1) / kRopeThreads;
+    return (int)(ctas < 148 * 2 ? ctas : 148 * 2);
+}
+
 template <bool BWD, typename T, int V, int G, int SL>
-inline cudaError_t rope_go(const RopeParams& p, dim3 grid, cudaStream_t stream) {
-    if constexpr (BWD) return launch_pdl(qk_norm_rope_bwd_kernel<T, V, G, SL>, grid, dim3(kRopeThreads), 0, stream, p);
-    return launch_pdl(qk_norm_rope_kernel<T, V, G, SL>, grid, dim3(kRopeThreads), 0, stream, p);
+inline cudaError_t rope_go(const RopeParams& p, int ctas, cudaStream_t stream) {
+    if constexpr (BWD) {
+        const int sums = kRopeThreads / G * p.dim * (int)sizeof(float), smem = std::max(rope_ring_bytes<V>(kRopeAheadBwd, 4), sums);
+        auto kernel = qk_norm_rope_bwd_kernel<T, V, G, SL>;
+        if (prepare_kernel_smem(reinterpret_cast<const void*>(kernel), smem) != 0) return cudaErrorInvalidValue;
+        return launch_pdl(kernel, dim3((unsigned)ctas, 2), dim3(kRopeThreads), (size_t)smem, stream, p);
+    } else {
+        const long long n = ((long long)p.tokens * p.split * G + kRopeThreads - 1) / kRopeThreads;
+        return launch_pdl(qk_norm_rope_kernel<T, V, G, SL>, dim3((unsigned)n), dim3(kRopeThreads),
+                          (size_t)rope_ring_bytes<V>(kRopeAhead, 2), stream, p);
+    }
 }
 
+// ctas: of the gradient kernel, per operand.
 template <bool BWD, typename T>
-inline cudaError_t rope_launch(const RopeParams& p, dim3 grid, cudaStream_t stream) {
+inline cudaError_t rope_launch(const RopeParams& p, int ctas, cudaStream_t stream) {
     constexpr int V = 16 / (int)sizeof(T);
-    if (!rope_wide(p, (int)sizeof(T), BWD)) return rope_go<BWD, T, 1, 32, 4>(p, grid, stream);
-    const int slots = (p.dim / V + 1) / 2;
-    if (slots <= 4) return rope_go<BWD, T, V, 4, 1>(p, grid, stream);
-    if (slots <= 8) return rope_go<BWD, T, V, 8, 1>(p, grid, stream);
-    if (slots <= 16) return rope_go<BWD, T, V, 16, 1>(p, grid, stream);
-    return rope_go<BWD, T, V, 32, 1>(p, grid, stream);
-}
-
-// CTAs per operand of the gradient kernel: a few per SM, each walking over many tokens, so that the weight
-// gradients leave few partial sums.  Depends on the sizes only.
-inline int rope_bwd_ctas(int tokens) {
-    const int steps = (tokens + kRopeTok - 1) / kRopeTok;
-    return steps < 148 * 4 ? steps : 148 * 4;
+    if (!rope_wide(p, (int)sizeof(T), BWD)) return rope_go<BWD, T, 1, 32, 4>(p, ctas, stream);
+    switch (rope_lanes(p, (int)sizeof(T), BWD)) {
+        case 4: return rope_go<BWD, T, V, 4, 1>(p, ctas, stream);
+        case 8: return rope_go<BWD, T, V, 8, 1>(p, ctas, stream);
+        case 16: return rope_go<BWD, T, V, 16, 1>(p, ctas, stream);
+        default: return rope_go<BWD, T, V, 32, 1>(p, ctas, stream);
+    }
 }
 
 }  // namespace r2l
