@@ -35,7 +35,8 @@ struct LaPass {
 __device__ __forceinline__ float la_clamp_decay(float g) { return g < -1e4f ? -1e4f : g; }
 
 // e^(g n) in fp32 from the exact product g n (the product's rounding error is put back to first order).
-__device__ __forceinline__ float la_decay_pow(float g, float n) {
+// Not inlined: it is for tables that are built once a head.
+__device__ __noinline__ float la_decay_pow(float g, float n) {
     const float x = g * n;
     const float e = expf(x);
     return fmaf(e, fmaf(g, n, -x), e);

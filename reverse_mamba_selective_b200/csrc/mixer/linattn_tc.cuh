@@ -156,6 +156,12 @@ __device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || la_wait_long(bar, parity);
 }
 
+// One arrival for the whole warp, behind all of its lanes' work (an arrival a lane costs a turn in the barrier unit each).
+__device__ __forceinline__ void la_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // Whether the phase with the given parity has completed; never suspends the warp (try_wait may, for microseconds).
 __device__ __forceinline__ bool la_test(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
@@ -175,7 +181,6 @@ struct LaItem {
     const float* in;   // state before chunk a, or NULL
     float* out;        // state after chunk b - 1, or NULL
     bool in_t, out_t;
-    float g;
 };
 
 // This CTA's share of the work: [begin, end).
@@ -214,7 +219,6 @@ __device__ __forceinline__ LaItem la_item(const TcLaunch& L, int work) {
         it.out = p.h_last + i * dd;
         it.out_t = p.h_t != 0;
     }
-    it.g = la_clamp_decay(p.log_decay[it.h]);
     return it;
 }
 
@@ -262,7 +266,7 @@ __device__ __forceinline__ bool la_not_finite(uint32_t m) { return (m & 0x7F80u)
 
 // Rows n .. of a chunk's V tile become zero (they stand behind the sequence's length: whatever they hold must
 // not meet a zero weight).
-__device__ __forceinline__ void la_zero_rows(unsigned char* v, int vb, int n, int tid, int nthreads) {
+__device__ __noinline__ void la_zero_rows(unsigned char* v, int vb, int n, int tid, int nthreads) {
     const int per = (kLaTok - n) * 8;
     for (int u = tid; u < vb * per; u += nthreads) {
         const int b = u / per, r = u - b * per;
@@ -281,35 +285,47 @@ __device__ __forceinline__ void la_add_inter(uint32_t (&r)[32], const uint32_t (
     }
 }
 
-// The outputs of 16 channels that came out not finite: a masked token may have met a zero weight.  The sum over the
-// unmasked pairs alone, from the swizzled tiles of P (two parts) and V, plus the state's part (oi: its accumulator, 0 where
-// there is none; fac: the tokens' factors).  Thread t's fragment, as tc_ld_frag_issue lays it out.  Not inlined: it is for
-// chunks with infinities or NaN only, and the code around it has to stay in the instruction cache.
-__device__ __noinline__ void la_redo(uint32_t* out, const unsigned char* pt, const unsigned char* vt, uint32_t oi, const float* fac,
-                                     int ch0, int n, int reverse) {
+// Not inlined, as all code off the usual path: the roles' loops together have to stay in the instruction cache.
+// What an epilogue warp does out of the ordinary for its 16 channels (from ch0 of the head), on a thread's fragment `out`:
+//  - outputs that came out not finite (redo): a masked token may have met a zero weight.  The sum over the unmasked pairs
+//    alone, from the swizzled tiles of P (two parts) and V, plus the state's part (oi: its accumulator, 0 where there is none;
+//    fac: the tokens' factors);
+//  - rows past the length become zeros;
+//  - fp32 outputs are stored.
+__device__ __noinline__ void la_finish(uint32_t* out, bool redo, const unsigned char* pt, const unsigned char* vt, uint32_t oi,
+                                       const float* fac, int ch0, int n, const LaPass& p, int seq, int h, int row0) {
     const int lane = threadIdx.x & 31, fr = lane >> 2, fc = (lane & 3) * 2;
-    uint32_t s2[32];
-    if (oi) {
-        tc_ld_frag_issue(oi, s2);
-        tc_wait_ld32(s2);
+    if (redo) {
+        uint32_t s2[32];
+        if (oi) {
+            tc_ld_frag_issue(oi, s2);
+            tc_wait_ld32(s2);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) out[e] = s2[e];
+            for (int e = 0; e < 32; ++e) out[e] = s2[e];
+        }
+#pragma unroll 1
+        for (int e = 0; e < 32; ++e) {
+            const int i = 8 * (e >> 2) + fc + (e & 1), ch = (ch0 & 63) + fr + 8 * ((e >> 1) & 1);
+            const int j0 = p.reverse ? i : 0, j1 = i >= n ? 0 : p.reverse ? n : i + 1;
+            float acc = 0.f;
+#pragma unroll 1
+            for (int j = j0; j < j1; ++j) {
+                const unsigned char* pa = pt + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2;
+                const float pw = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(pa)) +
+                                 __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(pa + kLaBlock));
+                const float vv = __bfloat162float(
+                    *reinterpret_cast<const __nv_bfloat16*>(vt + j * 128 + (((ch >> 3) ^ (j & 7)) << 4) + (ch & 7) * 2));
+                acc = fmaf(pw, vv, acc);
+            }
+            out[e] = __float_as_uint(oi ? fmaf(fac[i], __uint_as_float(out[e]), acc) : acc);
+        }
     }
+    float* y = static_cast<float*>(p.y) + ((size_t)seq * p.seq_len + row0) * p.y_tok + (size_t)h * p.dv + ch0 + fr;
 #pragma unroll 1
     for (int e = 0; e < 32; ++e) {
-        const int i = 8 * (e >> 2) + fc + (e & 1), ch = ch0 + fr + 8 * ((e >> 1) & 1);
-        const int j0 = reverse ? i : 0, j1 = i >= n ? 0 : reverse ? n : i + 1;
-        float acc = 0.f;
-#pragma unroll 1
-        for (int j = j0; j < j1; ++j) {
-            const unsigned char* pa = pt + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2;
-            const float pw = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(pa)) +
-                             __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(pa + kLaBlock));
-            const float vv = __bfloat162float(
-                *reinterpret_cast<const __nv_bfloat16*>(vt + j * 128 + (((ch >> 3) ^ (j & 7)) << 4) + (ch & 7) * 2));
-            acc = fmaf(pw, vv, acc);
-        }
-        out[e] = __float_as_uint(oi ? fmaf(fac[i], __uint_as_float(out[e]), acc) : acc);
+        const int i = 8 * (e >> 2) + fc + (e & 1), ch = 8 * ((e >> 1) & 1);
+        if (i >= n) out[e] = 0u;
+        if (p.y_f32 && row0 + i < p.seq_len && ch0 + fr + ch < p.dv) y[(size_t)i * p.y_tok + ch] = __uint_as_float(out[e]);
     }
 }
 
@@ -346,19 +362,19 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], Y ? 5 : 1);  // the last MMA, and the four epilogue warps
-            mbar_init(&kt_full[i], 256);
+            mbar_init(&kt_full[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&qk_full[i], 1);
-            mbar_init(&qk_empty[i], 64);
-            mbar_init(&p_full[i], 64);
+            mbar_init(&qk_empty[i], 2);
+            mbar_init(&p_full[i], 2);
             mbar_init(&p_empty[i], 4);
         }
         mbar_init(kv_full, 1);
-        mbar_init(s_full, 256);
+        mbar_init(s_full, 8);
         mbar_init(qs_done, 1);
         mbar_init(o_full, 1);
-        mbar_init(o_empty, 128);
+        mbar_init(o_empty, 4);
         fence_mbar_init();
         s_abort = 0;
     }
@@ -419,11 +435,6 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         const uint32_t dq = la_k_desc(smem_addr(smem)), dk = la_k_desc(smem_addr(smem + Cfg::QBytes));
         const uint32_t dv = la_mn_desc(smem_addr(smem + Cfg::QBytes + Cfg::KBytes));
         const uint32_t dkt = la_mn_desc(smem_addr(kt)), dp = la_k_desc(smem_addr(pbuf));
-        uint32_t total = 0;
-        for (int work = work0; work < work1; ++work) {
-            const LaItem it = la_item<Y>(L, work);
-            total += (uint32_t)(it.b - it.a);
-        }
         auto stage_off = [&](uint32_t pos) { return (pos % NST) * (uint32_t)(Cfg::StageBytes >> 4); };
         // scores of the chunk at `pos`, whose tiles have landed
         auto scores = [&](uint32_t pos) -> bool {
@@ -459,9 +470,9 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     if (elect_one()) {
 #pragma unroll
                         for (int part = 0; part < 3; ++part)
+                            if (part < 2 || L.nsplit > 2)
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                if (part < 2 || L.nsplit > 2)
+                                for (int kk = 0; kk < 4; ++kk)
                                     la_mma(tmem + Cfg::KV, dv + so + (kk * 2048 >> 4), dkt + ((part * Cfg::KBytes + kk * 2048) >> 4),
                                            kDesc | kMnA | kMnB | n_dk, part > 0 || kk > 0);
                         tc_commit(kv_full);
@@ -470,8 +481,8 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     __syncwarp();
                 }
                 if (Y) {
-                    // the next chunk's scores early, if its tiles are there
-                    if (pos + 1 < total && la_test(&full[(pos + 1) % NST], ((pos + 1) / NST) & 1u)) {
+                    // the next chunk's scores early, if its tiles are there (behind the last chunk they never are)
+                    if (la_test(&full[(pos + 1) % NST], ((pos + 1) / NST) & 1u)) {
                         if (!(ok = scores(pos + 1))) break;
                         nqk = pos + 2;
                     }
@@ -523,6 +534,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         // thread scales
         float dhi = 0.f, dlo = 0.f, kw[2] = {0.f, 0.f};
         int head = -1, kw_n = -1;
+        float g = 0.f;
         uint32_t pos = 0, nkv = 0, nqs = 0;
         for (int work = work0; work < work1 && ok; ++work) {
             const LaItem it = la_item<Y>(L, work);
@@ -547,6 +559,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
             }
             if (it.h != head) {
                 head = it.h;
+                g = la_clamp_decay(p.log_decay[head]);
                 kw_n = -1;
             }
             for (int c = it.a; c < it.b; ++c, ++pos) {
@@ -559,11 +572,11 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     unsigned char* s = smem + st * Cfg::StageBytes;
                     if (n != kw_n) {
                         kw_n = n;
-                        la_decay_pair(it.g, (float)n, dhi, dlo);
+                        la_decay_pair(g, (float)n, dhi, dlo);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int j = (tid >> 3) + 32 * e;
-                            kw[e] = j < n ? p.s_in * la_decay_pow(it.g, (float)((p.reverse ? j : n - 1 - j) + p.shift)) : 0.f;
+                            kw[e] = j < n ? p.s_in * la_decay_pow(g, (float)((p.reverse ? j : n - 1 - j) + p.shift)) : 0.f;
                         }
                     }
                     // K~: the swizzle only permutes 16-byte pieces within a token's row.  Piece tid + 256 m belongs to token
@@ -594,7 +607,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     if (n < kLaTok && row0 + n < p.seq_len) la_zero_rows(s + Cfg::QBytes + Cfg::KBytes, Cfg::VB, n, tid, 256);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                mbar_arrive(&kt_full[st]);
+                la_arrive(&kt_full[st]);
                 if (Y && has) {
                     // the operand copy of S, once the previous chunk's product has read the last one
                     if (!(ok = la_wait(qs_done, (nqs & 1u) ^ 1u))) break;
@@ -618,7 +631,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                         tc_wait_st();
                     }
                     tc_fence_before();
-                    mbar_arrive(s_full);
+                    la_arrive(s_full);
                     ++nqs;
                 }
                 if (need) {
@@ -661,14 +674,16 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         const int quarter = warp & 3, c0 = quarter * 32;  // this warp's channels c0 .. c0 + 31
         const uint32_t lane_off = (uint32_t)c0 << 16;
         const bool used = c0 < p.dv;                      // warp-uniform
-        const int fr = lane >> 2, fc = (lane & 3) * 2;    // this thread's row and column of an 8 x 8 fragment
+        const int fc = (lane & 3) * 2;                    // this thread's column of an 8 x 8 fragment
         float2 fac[8];  // s_out gamma^(position + 1 - shift) of tokens 8 k + fc, 8 k + fc + 1, for the head and chunk length
         int head = -1, fac_n = -1;
+        float g = 0.f;
         uint32_t pos = 0;
         for (int work = work0; work < work1 && ok; ++work) {
             const LaItem it = la_item<Y>(L, work);
             if (it.h != head) {
                 head = it.h;
+                g = la_clamp_decay(p.log_decay[head]);
                 fac_n = -1;
             }
             for (int c = it.a; c < it.b; ++c, ++pos) {
@@ -681,7 +696,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     __syncwarp();
 #pragma unroll
                     for (int i = lane; i < kLaTok; i += 32)
-                        wtab[i] = i < n ? p.s_out * la_decay_pow(it.g, (float)((p.reverse ? n - 1 - i : i) + 1 - p.shift)) : 0.f;
+                        wtab[i] = i < n ? p.s_out * la_decay_pow(g, (float)((p.reverse ? n - 1 - i : i) + 1 - p.shift)) : 0.f;
                     __syncwarp();
 #pragma unroll
                     for (int k = 0; k < 8; ++k) fac[k] = *reinterpret_cast<const float2*>(wtab + 8 * k + fc);
@@ -710,39 +725,26 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                             big = la_absmax_bf16x2(big, w[half][k]);
                         }
                         const bool redo = __any_sync(0xffffffffu, la_not_finite(big));
-                        if (redo || n != kLaTok || p.y_f32) {
+                        if (redo || row0 + n < min(row0 + kLaTok, p.seq_len) || p.y_f32) {
                             if (redo) {
                                 la_wait(&p_full[pos & 1], (pos >> 1) & 1u);
                                 la_wait(&full[st], (pos / NST) & 1u);
-                                uint32_t again[32];
-                                la_redo(again, pbuf + (pos & 1) * 2 * Cfg::PPart,
-                                        smem + st * Cfg::StageBytes + Cfg::QBytes + Cfg::KBytes + (c0 >> 6) * kLaBlock,
-                                        has ? ta + Cfg::OI : 0u, wtab, (c0 & 63) + half * 16, n, p.reverse);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) r[e] = again[e];
                             }
+                            uint32_t out[32];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)  // rows past the length are stored as zeros (past seq_len: not at all)
-                                if (8 * (e >> 2) + fc + (e & 1) >= n) r[e] = 0u;
-                            if (p.y_f32) {
-                                float* y = static_cast<float*>(p.y) + ((size_t)it.seq * p.seq_len + row0 + fc) * p.y_tok +
-                                           (size_t)it.h * p.dv + c0 + half * 16 + fr;
-#pragma unroll
-                                for (int k = 0; k < 8; ++k, y += 8 * p.y_tok)
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if (row0 + 8 * k + fc + (e & 1) < p.seq_len && c0 + half * 16 + fr + 8 * (e >> 1) < p.dv)
-                                            y[(e & 1) * p.y_tok + 8 * (e >> 1)] = __uint_as_float(r[4 * k + e]);
-                            }
+                            for (int e = 0; e < 32; ++e) out[e] = r[e];
+                            la_finish(out, redo, pbuf + (pos & 1) * 2 * Cfg::PPart,
+                                      smem + st * Cfg::StageBytes + Cfg::QBytes + Cfg::KBytes + (c0 >> 6) * kLaBlock,
+                                      has ? ta + Cfg::OI : 0u, wtab, c0 + half * 16, n, p, it.seq, it.h, row0);
 #pragma unroll
                             for (int k = 0; k < 16; ++k)
-                                w[half][k] = pack_bf16x2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+                                w[half][k] = pack_bf16x2(__uint_as_float(out[2 * k]), __uint_as_float(out[2 * k + 1]));
                         }
                     }
                 }
                 // both accumulators, P and V have been read
                 tc_fence_before();
-                mbar_arrive(o_empty);
+                la_arrive(o_empty);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_empty[pos & 1]);
                 if (used && !p.y_f32) {
@@ -770,13 +772,13 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                 if (lane == 0) mbar_arrive(&empty[st]);
             }
             if (it.a == 0 && ok) {  // chunks that lie wholly behind the row's tokens: zeros
-                const int ch = c0 + lane;
-                for (int t = it.nch * kLaTok; t < p.seq_len && ch < p.dv; ++t) {
-                    const size_t o = ((size_t)it.seq * p.seq_len + t) * p.y_tok + (size_t)it.h * p.dv + ch;
-                    if (p.y_f32)
-                        static_cast<float*>(p.y)[o] = 0.f;
-                    else
-                        static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(0.f);
+                // 16-byte pieces, the four warps' threads over rows and pieces (dv is a multiple of 8)
+                const int es = p.y_f32 ? 4 : 2, per_row = p.dv * es / 16, t0 = it.nch * kLaTok;
+                unsigned char* y = static_cast<unsigned char*>(p.y) +
+                                   (((size_t)it.seq * p.seq_len + t0) * p.y_tok + (size_t)it.h * p.dv) * es;
+                for (int i = tid - 256; i < (p.seq_len - t0) * per_row; i += 128) {
+                    const int t = i / per_row;
+                    *reinterpret_cast<uint4*>(y + (size_t)t * p.y_tok * es + (i - t * per_row) * 16) = make_uint4(0, 0, 0, 0);
                 }
             }
         }
@@ -798,14 +800,16 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         // weights of this row, for the head at hand: on the diagonal block, and on the full one (its columns are farther)
         float2 wd[16], wo[16];
         int head = -1;
+        float g = 0.f;
         uint32_t pos = 0;
         for (int work = work0; work < work1 && ok; ++work) {
             const LaItem it = la_item<Y>(L, work);
             if (it.b > it.a && it.h != head) {
                 head = it.h;
+                g = la_clamp_decay(p.log_decay[head]);
                 __syncwarp();
-                wtab[lane] = s * la_decay_pow(it.g, (float)lane);
-                wtab[lane + 32] = s * la_decay_pow(it.g, (float)(lane + 32));
+                wtab[lane] = s * la_decay_pow(g, (float)lane);
+                wtab[lane + 32] = s * la_decay_pow(g, (float)(lane + 32));
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
@@ -850,14 +854,14 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     put(32 * (1 - w), wo);
                 }
                 tc_fence_before();
-                mbar_arrive(&qk_empty[pos & 1]);
+                la_arrive(&qk_empty[pos & 1]);
                 if (n < kLaTok && row0 + n < p.seq_len) {
                     const int st = pos % NST;
                     if (!(ok = la_wait(&full[st], (pos / NST) & 1u))) break;
                     la_zero_rows(smem + st * Cfg::StageBytes + Cfg::QBytes + Cfg::KBytes, Cfg::VB, n, i, 64);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive(&p_full[pos & 1]);
+                la_arrive(&p_full[pos & 1]);
             }
         }
     }
@@ -931,15 +935,14 @@ inline bool la_encode(CUtensorMap* out, const void* base, int d, int heads, int 
     return false;
 }
 
-// How a pass is divided: segments per sequence and chunks in each.  Sequences are divided when there are fewer
-// (sequence, head) pairs than half the SMs, into as many segments as fill them, of four chunks at least: dividing
-// reads k and v a second time.
+// How a pass is divided: segments per sequence and chunks in each.  Few (sequence, head) pairs are divided into as many
+// segments as fill the SMs, of four chunks at least.  Dividing runs the state part of a chunk (about 0.7 of its time) twice and
+// adds two launches and the segments' states (about 10 us): n segments pay from (1 - 1.7 / n) nch chunk times (2 us) on.
 inline void la_segments(int nseq, int heads, int seq_len, int nsm, int& nseg, int& seg_chunks) {
     const long long items = (long long)nseq * heads;
     const int nch = (seq_len + kLaTok - 1) / kLaTok;
-    nseg = 1;
-    if (items > 0 && 2 * items <= nsm) nseg = (int)std::min<long long>(nsm / items, nch / 4);
-    if (nseg < 2) nseg = 1;
+    nseg = items > 0 ? (int)std::min<long long>(nsm / items, nch / 4) : 1;
+    if (nseg < 2 || (10 * nseg - 17) * nch < 50 * nseg) nseg = 1;
     seg_chunks = (nch + nseg - 1) / nseg;
     nseg = seg_chunks > 0 ? (nch + seg_chunks - 1) / seg_chunks : 1;
 }
