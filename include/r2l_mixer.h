@@ -96,7 +96,8 @@ R2L_API size_t r2l_linattn_bwd_workspace_size(const r2l_linattn_args *a);
  * dh_last = dL/dh_last (fp32, NULL = zero).  Writes dq, dk, dv (dtype, dense, shaped as q, k, v; the
  * gradients of shared heads are summed in fp32 before they are rounded) and, unless it is NULL,
  * dh0 = dL/dh0 (fp32).  Tokens past seq_lens get zero gradients.  log_decay is a fixed schedule and
- * gets none.  Every output is overwritten; no atomics, so results are the same from run to run.
+ * gets none.  Every output is overwritten and must overlap no input and no other output (dh0 being h0 or
+ * dh_last is refused); no atomics, so results are the same from run to run.
  */
 R2L_API r2l_status r2l_linattn_bwd(const r2l_linattn_args *a, const void *dy, const float *h0, const float *dh_last,
                                    void *dq, void *dk, void *dv, float *dh0, void *workspace, size_t workspace_bytes,

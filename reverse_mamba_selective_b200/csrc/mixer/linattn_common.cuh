@@ -35,22 +35,24 @@ struct LaPass {
 __device__ __forceinline__ float la_clamp_decay(float g) { return g < -1e4f ? -1e4f : g; }
 
 // e^(g n) in fp32 from the exact product g n (the product's rounding error is put back to first order).
-// Not inlined: it is for tables that are built once a head.
-__device__ __noinline__ float la_decay_pow(float g, float n) {
+__device__ __forceinline__ float la_decay_pow_of(float g, float n) {
     const float x = g * n;
     const float e = expf(x);
     return fmaf(e, fmaf(g, n, -x), e);
 }
+// Not inlined: for tables that are built once a head.
+__device__ __noinline__ float la_decay_pow(float g, float n) { return la_decay_pow_of(g, n); }
 
 // e^(g n) as the sum of two fp32 numbers: a state that is multiplied by it thousands of times keeps fp32
 // precision (one fp32 factor is 2^-25 off, the same way each time: 2.4e-4 after 8192 tokens).
-__device__ __noinline__ float2 la_decay_pair_of(float g, float n) {
+__device__ __forceinline__ float2 la_decay_pair_of(float g, float n) {
     const double e = exp((double)g * (double)n);
     const float hi = (float)e;
     return make_float2(hi, (float)(e - (double)hi));
 }
+__device__ __noinline__ float2 la_decay_pair_call(float g, float n) { return la_decay_pair_of(g, n); }
 __device__ __forceinline__ void la_decay_pair(float g, float n, float& hi, float& lo) {
-    const float2 e = la_decay_pair_of(g, n);
+    const float2 e = la_decay_pair_call(g, n);
     hi = e.x;
     lo = e.y;
 }

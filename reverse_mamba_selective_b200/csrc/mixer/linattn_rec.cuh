@@ -1,5 +1,5 @@
-// linattn_rec.cuh -- linear attention token by token, the state in registers: fp32 inputs, single tokens
-// (the serving step) and runs of a few tokens.
+// linattn_rec.cuh -- linear attention token by token, the state in registers: runs of fp32 inputs, and single tokens of
+// either type (the serving step).
 //
 // One CTA of 256 threads owns 4 TPR value columns of one (sequence, head): the state slice lies in registers,
 // a thread holding four neighbouring columns of every (256 / TPR)-th row.  Per token and state element: t = k v,
@@ -27,18 +27,7 @@ struct LaPasses {
     LaPass p[3];
 };
 
-__device__ __forceinline__ void la_store(const LaPass& p, size_t at, float v, float) {
-    (void)p.y_f32;
-    static_cast<float*>(p.y)[at] = v;
-}
-__device__ __forceinline__ void la_store(const LaPass& p, size_t at, float v, __nv_bfloat16) {
-    if (p.y_f32)
-        static_cast<float*>(p.y)[at] = v;
-    else
-        static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v);
-}
-
-template <typename T, int TPR>
+template <int TPR>
 __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_constant__ LaPasses passes) {
     constexpr int COLS = 4 * TPR, ROWS = kRecThreads / TPR, M = kRecMaxD / ROWS, W = 32 / TPR;  // W: rows a warp holds at once
     constexpr int J = kRecMaxD / 32, JV = (COLS + 31) / 32;
@@ -59,10 +48,10 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_c
     const int seq = (int)(item / p.heads), h = (int)(item - (long long)seq * p.heads);
     const int len = la_len(p, seq);
     const size_t tok0 = (size_t)seq * p.seq_len;
-    const T* q = static_cast<const T*>(p.q) + tok0 * p.q_tok + (size_t)(h / p.q_div) * p.dk;
-    const T* k = static_cast<const T*>(p.k) + tok0 * p.k_tok + (size_t)(h / p.k_div) * p.dk;
-    const T* v = static_cast<const T*>(p.v) + tok0 * p.v_tok + (size_t)(h / p.v_div) * p.dv + c0;
-    const size_t y0 = tok0 * p.y_tok + (size_t)h * p.dv + c0;
+    const float* q = static_cast<const float*>(p.q) + tok0 * p.q_tok + (size_t)(h / p.q_div) * p.dk;
+    const float* k = static_cast<const float*>(p.k) + tok0 * p.k_tok + (size_t)(h / p.k_div) * p.dk;
+    const float* v = static_cast<const float*>(p.v) + tok0 * p.v_tok + (size_t)(h / p.v_div) * p.dv + c0;
+    float* y = static_cast<float*>(p.y) + tok0 * p.y_tok + (size_t)h * p.dv + c0;
 
     const size_t sbase = (size_t)item * p.dk * p.dv;
     float4 s[M];
@@ -87,13 +76,13 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_c
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const int r = lane + 32 * j;
-            fq[j] = live && r < p.dk ? to_f32(q[(size_t)t * p.q_tok + r]) : 0.f;
-            fk[j] = live && r < p.dk ? to_f32(k[(size_t)t * p.k_tok + r]) : 0.f;
+            fq[j] = live && r < p.dk ? q[(size_t)t * p.q_tok + r] : 0.f;
+            fk[j] = live && r < p.dk ? k[(size_t)t * p.k_tok + r] : 0.f;
         }
 #pragma unroll
         for (int j = 0; j < JV; ++j) {
             const int c = lane + 32 * j;
-            fv[j] = live && c < ncol ? to_f32(v[(size_t)t * p.v_tok + c]) : 0.f;
+            fv[j] = live && c < ncol ? v[(size_t)t * p.v_tok + c] : 0.f;
         }
     };
     fetch(0);
@@ -165,14 +154,14 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_c
 #pragma unroll
                 for (int g = 0; g < kRecThreads / 32; ++g) o += part[tt][g][c];
                 const int t = p.reverse ? len - 1 - (n0 + tt) : n0 + tt;
-                la_store(p, y0 + (size_t)t * p.y_tok + c, o * p.s_out, T());
+                y[(size_t)t * p.y_tok + c] = o * p.s_out;
             }
         }
         // the staging of the next group writes sqk and sv, last read before the barrier above; `part` is written
         // again only behind the next group's first barrier
     }
     if (tid < ncol)
-        for (int t = len; t < p.seq_len; ++t) la_store(p, y0 + (size_t)t * p.y_tok + tid, 0.f, T());
+        for (int t = len; t < p.seq_len; ++t) y[(size_t)t * p.y_tok + tid] = 0.f;
     if (p.h_last && col_ok) {
 #pragma unroll
         for (int m = 0; m < M; ++m) {
@@ -268,7 +257,6 @@ __global__ void __launch_bounds__(kRecThreads, 4) linattn_step_kernel(const __gr
 
 // `n` passes over the same sequences and heads in one launch.  Columns per CTA: as many as the widest pass has when the
 // (sequence, head) pairs fill the GPU, fewer (down to 16) when few heads have to spread over the SMs.
-template <typename T>
 inline cudaError_t linattn_rec_launch(const LaPass* p, int n, int nsm, cudaStream_t stream) {
     LaPasses all;
     std::memset(&all, 0, sizeof(all));
@@ -282,10 +270,10 @@ inline cudaError_t linattn_rec_launch(const LaPass* p, int n, int nsm, cudaStrea
     while (tpr > 4 && (4 * tpr >= 2 * dv || items * n * ((dv + 4 * tpr - 1) / (4 * tpr)) < 2LL * nsm)) tpr >>= 1;
     const dim3 grid((unsigned)items, (unsigned)((dv + 4 * tpr - 1) / (4 * tpr)), (unsigned)n);
     switch (tpr) {
-        case 32: return launch_pdl(linattn_rec_kernel<T, 32>, grid, dim3(kRecThreads), 0, stream, all);
-        case 16: return launch_pdl(linattn_rec_kernel<T, 16>, grid, dim3(kRecThreads), 0, stream, all);
-        case 8: return launch_pdl(linattn_rec_kernel<T, 8>, grid, dim3(kRecThreads), 0, stream, all);
-        default: return launch_pdl(linattn_rec_kernel<T, 4>, grid, dim3(kRecThreads), 0, stream, all);
+        case 32: return launch_pdl(linattn_rec_kernel<32>, grid, dim3(kRecThreads), 0, stream, all);
+        case 16: return launch_pdl(linattn_rec_kernel<16>, grid, dim3(kRecThreads), 0, stream, all);
+        case 8: return launch_pdl(linattn_rec_kernel<8>, grid, dim3(kRecThreads), 0, stream, all);
+        default: return launch_pdl(linattn_rec_kernel<4>, grid, dim3(kRecThreads), 0, stream, all);
     }
 }
 

@@ -296,15 +296,14 @@ __device__ __noinline__ void la_finish(uint32_t* out, bool redo, const unsigned 
                                        const float* fac, int ch0, int n, const LaPass& p, int seq, int h, int row0) {
     const int lane = threadIdx.x & 31, fr = lane >> 2, fc = (lane & 3) * 2;
     if (redo) {
-        uint32_t s2[32];
+        uint32_t s2[32] = {};
         if (oi) {
             tc_ld_frag_issue(oi, s2);
             tc_wait_ld32(s2);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) out[e] = s2[e];
         }
 #pragma unroll 1
         for (int e = 0; e < 32; ++e) {
+            if ((out[e] & 0x7F800000u) != 0x7F800000u) continue;
             const int i = 8 * (e >> 2) + fc + (e & 1), ch = (ch0 & 63) + fr + 8 * ((e >> 1) & 1);
             const int j0 = p.reverse ? i : 0, j1 = i >= n ? 0 : p.reverse ? n : i + 1;
             float acc = 0.f;
@@ -317,7 +316,7 @@ __device__ __noinline__ void la_finish(uint32_t* out, bool redo, const unsigned 
                     *reinterpret_cast<const __nv_bfloat16*>(vt + j * 128 + (((ch >> 3) ^ (j & 7)) << 4) + (ch & 7) * 2));
                 acc = fmaf(pw, vv, acc);
             }
-            out[e] = __float_as_uint(oi ? fmaf(fac[i], __uint_as_float(out[e]), acc) : acc);
+            out[e] = __float_as_uint(oi ? fmaf(fac[i], __uint_as_float(s2[e]), acc) : acc);
         }
     }
     float* y = static_cast<float*>(p.y) + ((size_t)seq * p.seq_len + row0) * p.y_tok + (size_t)h * p.dv + ch0 + fr;
@@ -846,11 +845,19 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                 };
                 tc_ld32_issue(ta + 32 * w, r);
                 tc_wait_ld32(r);
+                // masked scores are zeros, not scores times zero: a key there may be infinite
+                const int left = n - 32 * w;  // columns inside the length
+                const uint32_t keep = (p.reverse ? ~0u << lane : 2u * (1u << lane) - 1u) & (left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = keep >> j & 1u ? r[j] : 0u;
                 if (!(ok = la_wait(&p_empty[pos & 1], ((pos >> 1) & 1u) ^ 1u))) break;
                 put(32 * w, wd);
                 if (full_block && n > 32) {
                     tc_ld32_issue(ta + 32 * (1 - w), r);
                     tc_wait_ld32(r);
+                    if (p.reverse && n < kLaTok)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = 32 + j < n ? r[j] : 0u;
                     put(32 * (1 - w), wo);
                 }
                 tc_fence_before();

@@ -8,6 +8,7 @@
 
 #include "r2l_mixer.h"
 #include "../common.cuh"
+#include "linattn_block.cuh"
 #include "linattn_common.cuh"
 #include "linattn_rec.cuh"
 #include "linattn_tc.cuh"
@@ -98,27 +99,28 @@ LaPass forward_pass(const r2l_linattn_args* a, const float* h0, float* h_last, v
     return p;
 }
 
-// bf16 runs of more than a few tokens go to the tensor cores, token by token otherwise.
-bool on_tensor_cores(r2l_dtype dtype, int seq_len) { return dtype == R2L_BF16 && seq_len > 8; }
-
 // Workspace of one pass (the states between a divided sequence's segments).
 size_t pass_bytes(const r2l_linattn_args* a) {
     const int nblk = a->reverse ? a->seqlen / a->block_len : 1, len = a->seqlen / nblk;
-    if (!on_tensor_cores(a->dtype, len)) return 0;
+    if (a->dtype != R2L_BF16) return 0;
     return align256(la_segment_bytes(a->batch * nblk, a->n_heads, len, a->d_k, a->d_v, sm_count()));
 }
 
-// `n` passes over the same sequences and heads; seg: pass_bytes bytes, used by one after another.
+// `n` passes over the same sequences and heads; seg: pass_bytes bytes, used by one after another.  fp32 runs token by
+// token; bf16 in chunks, short blocks by the kernels for them (the gradients of a block with a state transpose it,
+// which the resuming kernel does not).
 bool run_passes(const LaPass* p, int n, r2l_dtype dtype, void* seg, cudaStream_t stream) {
     const int nsm = sm_count();
-    if (on_tensor_cores(dtype, p->seq_len)) {
-        for (int i = 0; i < n; ++i)
-            if (!linattn_tc_launch(p[i], static_cast<float*>(seg), nsm, stream)) return false;
-        return true;
-    }
-    const cudaError_t e = dtype == R2L_F32 ? linattn_rec_launch<float>(p, n, nsm, stream)
-                                           : linattn_rec_launch<__nv_bfloat16>(p, n, nsm, stream);
-    return cuda_ok(e, "linear attention kernel launch");
+    if (dtype == R2L_F32) return cuda_ok(linattn_rec_launch(p, n, nsm, stream), "linear attention kernel launch");
+    bool state = false;
+    for (int i = 0; i < n; ++i) state = state || p[i].h0 || p[i].h_last;
+    if (!state && p->seq_len <= kBlkMaxTok)
+        return cuda_ok(linattn_block_launch(p, n, stream), "linear attention block kernel launch");
+    if (n == 1 && p->seq_len <= linattn_resume_max(*p))
+        return cuda_ok(linattn_resume_launch(*p, nsm, stream), "linear attention block kernel launch");
+    for (int i = 0; i < n; ++i)
+        if (!linattn_tc_launch(p[i], static_cast<float*>(seg), nsm, stream)) return false;
+    return true;
 }
 
 r2l_status copy_state(const float* h0, float* h_last, size_t n, cudaStream_t stream) {
@@ -197,6 +199,7 @@ r2l_status r2l_linattn_bwd(const r2l_linattn_args* a, const void* dy, const floa
     if (st != R2L_OK) return st;
     if ((h0 || dh_last || dh0) && !carries_state(a)) return R2L_ERR_INVALID_ARG;
     if (!aligned16(h0) || !aligned16(dh_last) || !aligned16(dh0)) return R2L_ERR_INVALID_ARG;
+    if (dh0 && (dh0 == dh_last || dh0 == h0)) return R2L_ERR_INVALID_ARG;
     if (la_empty(a)) return R2L_OK;
     if (a->seqlen == 0) return copy_state(dh_last, dh0, (size_t)a->batch * a->n_heads * a->d_k * a->d_v, stream);
     for (const void* q : {dy, (const void*)dq, (const void*)dk, (const void*)dv})

@@ -114,6 +114,13 @@ def test_linattn_output_and_state_refusals(r2l):
     assert step(la(r2l, **one), h=4100) == BAD
 
 
+def test_gradient_of_the_state_is_not_written_over_a_state(r2l):
+    lib = r2l.load_mixer()
+    grad = lambda h0, dh, dh0: code(r2l, lib.r2l_linattn_bwd(
+        ctypes.byref(la(r2l)), 16384, h0, dh, 32768, 65536, 131072, dh0, 1 << 20, 1 << 40, None))
+    assert grad(4096, 8192, 4096) == BAD and grad(4096, 8192, 8192) == BAD and grad(None, 8192, 8192) == BAD
+
+
 def test_empty_problems_are_noops(r2l):
     lib = r2l.load_mixer()
     for over in (dict(batch=0), dict(n_heads=0), dict(d_k=0), dict(d_v=0), dict(seqlen=0)):
