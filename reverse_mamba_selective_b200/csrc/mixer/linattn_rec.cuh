@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "linattn_common.cuh"
 
@@ -27,11 +28,13 @@ struct LaPasses {
     LaPass p[3];
 };
 
-template <int TPR>
+// DK: 64 or 128, the passes' key channels at most.
+template <int TPR, int DK>
 __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_constant__ LaPasses passes) {
-    constexpr int COLS = 4 * TPR, ROWS = kRecThreads / TPR, M = kRecMaxD / ROWS, W = 32 / TPR;  // W: rows a warp holds at once
-    constexpr int J = kRecMaxD / 32, JV = (COLS + 31) / 32;
-    __shared__ float2 sqk[kRecTok][kRecMaxD];
+    constexpr int COLS = 4 * TPR, ROWS = kRecThreads / TPR, M = DK / ROWS, W = 32 / TPR;  // W: rows a warp holds at once
+    constexpr int J = DK / 32, JV = (COLS + 31) / 32;
+    constexpr int U = M <= 2 ? 4 : 1;  // tokens in flight: a token of few rows is all latency
+    __shared__ float2 sqk[kRecTok][DK];
     __shared__ __align__(16) float sv[kRecTok][COLS];
     __shared__ __align__(16) float part[kRecTok][kRecThreads / 32][COLS];
     const LaPass& p = passes.p[blockIdx.z];
@@ -98,54 +101,61 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_c
             if (lane + 32 * j < COLS) sv[warp][lane + 32 * j] = fv[j];
         __syncthreads();
         fetch(n0 + kRecTok);
-        for (int tt = 0; tt < nt; ++tt) {
-            const float4 vv = *reinterpret_cast<const float4*>(&sv[tt][cq]);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto tokens = [&](auto shift) {
+            constexpr bool SHIFT = decltype(shift)::value;
+#pragma unroll U
+            for (int tt = 0; tt < nt; ++tt) {
+                const float4 vv = *reinterpret_cast<const float4*>(&sv[tt][cq]);
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int m = 0; m < M; ++m) {
-                if (m * ROWS >= p.dk) break;  // the same for the whole CTA; rows past dk hold zeros throughout
-                const float2 qk = sqk[tt][rr + m * ROWS];
-                float4 a = s[m];
-                if (p.shift) {
-                    a = make_float4(fmaf(qk.y, vv.x, a.x), fmaf(qk.y, vv.y, a.y), fmaf(qk.y, vv.z, a.z), fmaf(qk.y, vv.w, a.w));
+                for (int m = 0; m < M; ++m) {
+                    const float2 qk = sqk[tt][rr + m * ROWS];
+                    float4 a = s[m];
+                    if constexpr (SHIFT) {
+                        a = make_float4(fmaf(qk.y, vv.x, a.x), fmaf(qk.y, vv.y, a.y), fmaf(qk.y, vv.z, a.z), fmaf(qk.y, vv.w, a.w));
+                    } else {
+                        a.x = fmaf(a.x, ghi, fmaf(a.x, glo, qk.y * vv.x));
+                        a.y = fmaf(a.y, ghi, fmaf(a.y, glo, qk.y * vv.y));
+                        a.z = fmaf(a.z, ghi, fmaf(a.z, glo, qk.y * vv.z));
+                        a.w = fmaf(a.w, ghi, fmaf(a.w, glo, qk.y * vv.w));
+                    }
+                    o.x = fmaf(qk.x, a.x, o.x);
+                    o.y = fmaf(qk.x, a.y, o.y);
+                    o.z = fmaf(qk.x, a.z, o.z);
+                    o.w = fmaf(qk.x, a.w, o.w);
+                    if constexpr (SHIFT) {
+                        a.x = fmaf(a.x, ghi, a.x * glo);
+                        a.y = fmaf(a.y, ghi, a.y * glo);
+                        a.z = fmaf(a.z, ghi, a.z * glo);
+                        a.w = fmaf(a.w, ghi, a.w * glo);
+                    }
+                    s[m] = a;
+                }
+                // the warp's W rows: each step halves what a lane sums, down to one column a lane
+                if constexpr (W == 1) {
+                    *reinterpret_cast<float4*>(&part[tt][warp][cq]) = o;
                 } else {
-                    a.x = fmaf(a.x, ghi, fmaf(a.x, glo, qk.y * vv.x));
-                    a.y = fmaf(a.y, ghi, fmaf(a.y, glo, qk.y * vv.y));
-                    a.z = fmaf(a.z, ghi, fmaf(a.z, glo, qk.y * vv.z));
-                    a.w = fmaf(a.w, ghi, fmaf(a.w, glo, qk.y * vv.w));
-                }
-                o.x = fmaf(qk.x, a.x, o.x);
-                o.y = fmaf(qk.x, a.y, o.y);
-                o.z = fmaf(qk.x, a.z, o.z);
-                o.w = fmaf(qk.x, a.w, o.w);
-                if (p.shift) {
-                    a.x = fmaf(a.x, ghi, a.x * glo);
-                    a.y = fmaf(a.y, ghi, a.y * glo);
-                    a.z = fmaf(a.z, ghi, a.z * glo);
-                    a.w = fmaf(a.w, ghi, a.w * glo);
-                }
-                s[m] = a;
-            }
-            // the warp's W rows: each step halves what a lane sums, down to one column a lane
-            if constexpr (W == 1) {
-                *reinterpret_cast<float4*>(&part[tt][warp][cq]) = o;
-            } else {
-                const bool hi = lane & TPR;
-                const float sx = hi ? o.x : o.z, sy = hi ? o.y : o.w;
-                float2 u = hi ? make_float2(o.z, o.w) : make_float2(o.x, o.y);
-                u.x += __shfl_xor_sync(0xffffffffu, sx, TPR);
-                u.y += __shfl_xor_sync(0xffffffffu, sy, TPR);
-                if constexpr (W == 2) {
-                    *reinterpret_cast<float2*>(&part[tt][warp][cq + (hi ? 2 : 0)]) = u;
-                } else {
-                    const bool hi2 = lane & (2 * TPR);
-                    float w = hi2 ? u.y : u.x;
-                    w += __shfl_xor_sync(0xffffffffu, hi2 ? u.x : u.y, 2 * TPR);
-                    if constexpr (W == 8) w += __shfl_xor_sync(0xffffffffu, w, 4 * TPR);
-                    if (W == 4 || lane < 4 * TPR) part[tt][warp][cq + (hi ? 2 : 0) + (hi2 ? 1 : 0)] = w;
+                    const bool hi = lane & TPR;
+                    const float sx = hi ? o.x : o.z, sy = hi ? o.y : o.w;
+                    float2 u = hi ? make_float2(o.z, o.w) : make_float2(o.x, o.y);
+                    u.x += __shfl_xor_sync(0xffffffffu, sx, TPR);
+                    u.y += __shfl_xor_sync(0xffffffffu, sy, TPR);
+                    if constexpr (W == 2) {
+                        *reinterpret_cast<float2*>(&part[tt][warp][cq + (hi ? 2 : 0)]) = u;
+                    } else {
+                        const bool hi2 = lane & (2 * TPR);
+                        float w = hi2 ? u.y : u.x;
+                        w += __shfl_xor_sync(0xffffffffu, hi2 ? u.x : u.y, 2 * TPR);
+                        if constexpr (W == 8) w += __shfl_xor_sync(0xffffffffu, w, 4 * TPR);
+                        if (W == 4 || lane < 4 * TPR) part[tt][warp][cq + (hi ? 2 : 0) + (hi2 ? 1 : 0)] = w;
+                    }
                 }
             }
-        }
+        };
+        if (p.shift)
+            tokens(std::true_type());
+        else
+            tokens(std::false_type());
         __syncthreads();
         for (int i = tid; i < nt * COLS; i += kRecThreads) {
             const int tt = i / COLS, c = i % COLS;
@@ -260,20 +270,30 @@ __global__ void __launch_bounds__(kRecThreads, 4) linattn_step_kernel(const __gr
 inline cudaError_t linattn_rec_launch(const LaPass* p, int n, int nsm, cudaStream_t stream) {
     LaPasses all;
     std::memset(&all, 0, sizeof(all));
-    int dv = 0;
+    int dk = 0, dv = 0;
     for (int i = 0; i < n; ++i) {
         all.p[i] = p[i];
+        dk = std::max(dk, p[i].dk);
         dv = std::max(dv, p[i].dv);
     }
     const long long items = (long long)p[0].nseq * p[0].heads;
     int tpr = 32;
     while (tpr > 4 && (4 * tpr >= 2 * dv || items * n * ((dv + 4 * tpr - 1) / (4 * tpr)) < 2LL * nsm)) tpr >>= 1;
     const dim3 grid((unsigned)items, (unsigned)((dv + 4 * tpr - 1) / (4 * tpr)), (unsigned)n);
+    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kRecThreads), 0, stream, all); };
+    if (dk <= 64) {
+        switch (tpr) {
+            case 32: return go(linattn_rec_kernel<32, 64>);
+            case 16: return go(linattn_rec_kernel<16, 64>);
+            case 8: return go(linattn_rec_kernel<8, 64>);
+            default: return go(linattn_rec_kernel<4, 64>);
+        }
+    }
     switch (tpr) {
-        case 32: return launch_pdl(linattn_rec_kernel<32>, grid, dim3(kRecThreads), 0, stream, all);
-        case 16: return launch_pdl(linattn_rec_kernel<16>, grid, dim3(kRecThreads), 0, stream, all);
-        case 8: return launch_pdl(linattn_rec_kernel<8>, grid, dim3(kRecThreads), 0, stream, all);
-        default: return launch_pdl(linattn_rec_kernel<4>, grid, dim3(kRecThreads), 0, stream, all);
+        case 32: return go(linattn_rec_kernel<32, 128>);
+        case 16: return go(linattn_rec_kernel<16, 128>);
+        case 8: return go(linattn_rec_kernel<8, 128>);
+        default: return go(linattn_rec_kernel<4, 128>);
     }
 }
 

@@ -56,7 +56,7 @@ struct LaCfg {
     static constexpr int KB = DK / 64, VB = DV / 64;
     static constexpr int QBytes = Y ? KB * kLaBlock : 0, KBytes = KB * kLaBlock, VBytes = VB * kLaBlock;
     static constexpr int StageBytes = QBytes + KBytes + VBytes;
-    static constexpr int KtBytes = 3 * KBytes;
+    static constexpr int KtBuf = 3 * KBytes, KtBytes = Y ? KtBuf : 2 * KtBuf;
     static constexpr int PPart = kLaBlock, PBytes = Y ? 2 * 2 * PPart : 0;  // two buffers of two parts
     static constexpr int TabBytes = 6 * kLaTok * 4, BarBytes = 256;
     static constexpr int Fixed = 1024 /*alignment*/ + KtBytes + PBytes + TabBytes + BarBytes;
@@ -65,7 +65,7 @@ struct LaCfg {
     static constexpr int SmemBytes = Fixed + Stages * StageBytes;
     static_assert((3 * Stages + 13) * 8 <= BarBytes, "barriers");
     // tensor memory columns
-    static constexpr int QK = 0, OI = 128, OA = 192, KV = 256, SB = 384, Cols = 512;  // SB: two parts of DK / 2
+    static constexpr int QK = 0, OI = 128, OA = 192, KV = 256, SB = 384, Cols = 512;  // SB: two parts of DK / 2, or a second KV
     static_assert(Stages >= 2, "ring depth");
 };
 
@@ -467,14 +467,16 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                 if (need) {
                     tc_fence_after();
                     if (elect_one()) {
+                        const uint32_t b = Y ? 0 : pos & 1;  // the state pass has two of K~ and of KV
 #pragma unroll
                         for (int part = 0; part < 3; ++part)
                             if (part < 2 || L.nsplit > 2)
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
-                                    la_mma(tmem + Cfg::KV, dv + so + (kk * 2048 >> 4), dkt + ((part * Cfg::KBytes + kk * 2048) >> 4),
+                                    la_mma(tmem + Cfg::KV + b * 128, dv + so + (kk * 2048 >> 4),
+                                           dkt + b * (Cfg::KtBuf >> 4) + ((part * Cfg::KBytes + kk * 2048) >> 4),
                                            kDesc | kMnA | kMnB | n_dk, part > 0 || kk > 0);
-                        tc_commit(kv_full);
+                        tc_commit(Y ? kv_full : &qk_full[b]);
                         if (!Y) tc_commit(&empty[st]);
                     }
                     __syncwarp();
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
         // of the head and chunk length at hand: the chunk's decay, and the weights of the two tokens whose keys this
         // thread scales
         float dhi = 0.f, dlo = 0.f, kw[2] = {0.f, 0.f};
-        int head = -1, kw_n = -1;
+        int head = -1, kw_n = -1, d_n = -1;
         float g = 0.f;
         uint32_t pos = 0, nkv = 0, nqs = 0;
         for (int work = work0; work < work1 && ok; ++work) {
@@ -559,19 +561,18 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
             if (it.h != head) {
                 head = it.h;
                 g = la_clamp_decay(p.log_decay[head]);
-                kw_n = -1;
+                kw_n = d_n = -1;
             }
-            for (int c = it.a; c < it.b; ++c, ++pos) {
-                const bool has = it.in || c > it.a, need = c < it.b - 1 || it.out;
+            // K~ of the chunk c, the at-th of this CTA
+            auto keys = [&](int c, uint32_t at) -> bool {
                 int row0, n;
                 la_chunk(p, it, c, row0, n);
-                const int st = pos % NST;
-                if (!(ok = la_wait(&full[st], (pos / NST) & 1u))) break;
-                if (need) {
+                const int st = at % NST;
+                if (!la_wait(&full[st], (at / NST) & 1u)) return false;
+                if (c < it.b - 1 || it.out) {
                     unsigned char* s = smem + st * Cfg::StageBytes;
                     if (n != kw_n) {
                         kw_n = n;
-                        la_decay_pair(g, (float)n, dhi, dlo);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int j = (tid >> 3) + 32 * e;
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                         const uint32_t xs[4] = {x[m].x, x[m].y, x[m].z, x[m].w};
                         float2 a[4];
                         uint32_t t[4];
-                        unsigned char* o = kt + (tid + m * 256) * 16;
+                        unsigned char* o = kt + (Y ? 0 : (at & 1) * Cfg::KtBuf) + (tid + m * 256) * 16;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) a[e] = la_mul2(make_float2(la_bf16_lo(xs[e]), la_bf16_hi(xs[e])), w);
 #pragma unroll
@@ -607,6 +608,15 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 la_arrive(&kt_full[st]);
+                return true;
+            };
+            // the state pass, which has room for two, prepares the next chunk's before it waits for this one's product
+            if (!Y && it.a < it.b && !(ok = keys(it.a, pos))) break;
+            for (int c = it.a; c < it.b; ++c, ++pos) {
+                const bool has = it.in || c > it.a, need = c < it.b - 1 || it.out;
+                int row0, n;
+                la_chunk(p, it, c, row0, n);
+                if (Y ? !(ok = keys(c, pos)) : c + 1 < it.b && !(ok = keys(c + 1, pos + 1))) break;
                 if (Y && has) {
                     // the operand copy of S, once the previous chunk's product has read the last one
                     if (!(ok = la_wait(qs_done, (nqs & 1u) ^ 1u))) break;
@@ -634,14 +644,18 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                     ++nqs;
                 }
                 if (need) {
-                    if (!(ok = la_wait(kv_full, nkv & 1u))) break;
+                    if (!(ok = Y ? la_wait(kv_full, nkv & 1u) : la_wait(&qk_full[pos & 1], (pos >> 1) & 1u))) break;
                     ++nkv;
                     tc_fence_after();
+                    if (n != d_n) {
+                        d_n = n;
+                        la_decay_pair(g, (float)n, dhi, dlo);
+                    }
                     if (rows_used) {
 #pragma unroll
                         for (int q = 0; q < H / 32; ++q) {
                             uint32_t r[32];
-                            tc_ld32_issue(tmem + lane_off + Cfg::KV + k0 + q * 32, r);
+                            tc_ld32_issue(tmem + lane_off + Cfg::KV + (Y ? 0 : (pos & 1) * 128) + k0 + q * 32, r);
                             tc_wait_ld32(r);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
@@ -943,13 +957,14 @@ inline bool la_encode(CUtensorMap* out, const void* base, int d, int heads, int 
 }
 
 // How a pass is divided: segments per sequence and chunks in each.  Few (sequence, head) pairs are divided into as many
-// segments as fill the SMs, of four chunks at least.  Dividing runs the state part of a chunk (about 0.7 of its time) twice and
-// adds two launches and the segments' states (about 10 us): n segments pay from (1 - 1.7 / n) nch chunk times (2 us) on.
+// segments as fill the SMs, of four chunks at least.  Dividing runs the state part of a chunk (half its time) twice and
+// adds two launches and the segments' states (about 20 us): n segments pay from (1 - 1.55 / n) nch chunk times (2 us) on.
+// 64 pairs, n = 2, 32 chunks: 75 us undivided, 86 divided, equal at 48; 16 pairs, n = 9, 512 chunks: 1030 and 226 us.
 inline void la_segments(int nseq, int heads, int seq_len, int nsm, int& nseg, int& seg_chunks) {
     const long long items = (long long)nseq * heads;
     const int nch = (seq_len + kLaTok - 1) / kLaTok;
     nseg = items > 0 ? (int)std::min<long long>(nsm / items, nch / 4) : 1;
-    if (nseg < 2 || (10 * nseg - 17) * nch < 50 * nseg) nseg = 1;
+    if (nseg < 2 || (20 * nseg - 31) * nch < 200 * nseg) nseg = 1;
     seg_chunks = (nch + nseg - 1) / nseg;
     nseg = seg_chunks > 0 ? (nch + seg_chunks - 1) / seg_chunks : 1;
 }
