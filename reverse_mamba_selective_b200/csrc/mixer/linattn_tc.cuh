@@ -21,8 +21,16 @@
 //         Q (and K) tile and stored from there by TMA
 //   12-13 scores: QK -> P, 32 tokens a warp, in blocks of 32 x 32: one on the diagonal, one full, one zero
 //   14    TMA producer (ring of chunk tiles), 15 MMA issuer
-// Bound by memory for heads of 64 to 128: a chunk moves 64 KB (d = 128), 1.5 us of an SM's share of the
-// bandwidth, against 0.7 us of tensor time.
+// A chunk moves 64 KB (d = 128), 1.5 us of an SM's share of the bandwidth, against 0.7 us of tensor time.  What
+// bounds it is the chain through the state, 3.5 thousand cycles a chunk: K~ (1100, and 260 until the MMA may read it), the
+// split copy of S (800), KV's product and its way back (700), the rest waits; under a long run the 1000 W limit
+// lowers the clock as well.  128 heads and sequences of 4096 tokens: 147 us at 1.9 GHz (3.7 TB/s), 170 to 180 us back to
+// back at the limit.  Measured and not kept: V~ instead of K~ through tensor memory (224 us against 173), two issuing warps
+// (205), 30 warps of 64 registers (155 against 148), the next K~ held in registers (spills: 293), spinning waits (161
+// against 149), a truncating split (172 against 169).
+//
+// The pass over the states of a divided sequence (Y false) has room for two K~ and two KV: the next chunk's K~ is
+// made before this one's KV is waited for, 1.6 us a chunk instead of 2.0.
 //
 // Masked places never reach an output: rows of V past a sequence's length are zeroed, keys past it are not read into
 // K~, and where an output comes out not finite (a masked weight is a zero factor, and zero times an infinity is
@@ -34,6 +42,7 @@
 #include "../tc_common.cuh"
 #include "../tmap.cuh"
 #include "linattn_common.cuh"
+#include "pairs.cuh"
 
 namespace r2l {
 
@@ -229,30 +238,13 @@ __device__ __forceinline__ void la_chunk(const LaPass& p, const LaItem& it, int 
     n = min(kLaTok, it.len - row0);
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 la_fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(*reinterpret_cast<unsigned long long*>(&d))
-        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
-          "l"(*reinterpret_cast<unsigned long long*>(&c)));
-    return d;
-}
-__device__ __forceinline__ float2 la_mul2(float2 a, float2 b) {
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(*reinterpret_cast<unsigned long long*>(&d))
-        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-    return d;
-}
-
 __device__ __forceinline__ float la_bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float la_bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // x rounded to two bf16; x becomes what the rounding left (exact).
 __device__ __forceinline__ uint32_t la_split(float2& x) {
     const uint32_t w = pack_bf16x2(x.x, x.y);
-    x = la_fma2(make_float2(la_bf16_lo(w), la_bf16_hi(w)), make_float2(-1.f, -1.f), x);
+    x = fma2(make_float2(la_bf16_lo(w), la_bf16_hi(w)), make_float2(-1.f, -1.f), x);
     return w;
 }
 
@@ -278,7 +270,7 @@ __device__ __noinline__ void la_zero_rows(unsigned char* v, int vb, int n, int t
 __device__ __forceinline__ void la_add_inter(uint32_t (&r)[32], const uint32_t (&s2)[32], const float2 (&fac)[8]) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-        const float2 y = la_fma2(fac[k >> 1], make_float2(__uint_as_float(s2[2 * k]), __uint_as_float(s2[2 * k + 1])),
+        const float2 y = fma2(fac[k >> 1], make_float2(__uint_as_float(s2[2 * k]), __uint_as_float(s2[2 * k + 1])),
                                  make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])));
         r[2 * k] = __float_as_uint(y.x);
         r[2 * k + 1] = __float_as_uint(y.y);
@@ -595,7 +587,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                         uint32_t t[4];
                         unsigned char* o = kt + (Y ? 0 : (at & 1) * Cfg::KtBuf) + (tid + m * 256) * 16;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) a[e] = la_mul2(make_float2(la_bf16_lo(xs[e]), la_bf16_hi(xs[e])), w);
+                        for (int e = 0; e < 4; ++e) a[e] = mul2(make_float2(la_bf16_lo(xs[e]), la_bf16_hi(xs[e])), w);
 #pragma unroll
                         for (int part = 0; part < 3; ++part) {
                             if (part == 2 && L.nsplit < 3) break;
@@ -661,7 +653,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                             for (int e = 0; e < 16; ++e) {
                                 const float2 x = S[q * 16 + e];
                                 const float2 kv = make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-                                S[q * 16 + e] = la_fma2(x, make_float2(dhi, dhi), la_fma2(x, make_float2(dlo, dlo), kv));
+                                S[q * 16 + e] = fma2(x, make_float2(dhi, dhi), fma2(x, make_float2(dlo, dlo), kv));
                             }
                         }
                     }
@@ -847,7 +839,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                         uint32_t a[4], b[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            float2 x = la_mul2(make_float2(__uint_as_float(r[q * 8 + 2 * e]), __uint_as_float(r[q * 8 + 2 * e + 1])),
+                            float2 x = mul2(make_float2(__uint_as_float(r[q * 8 + 2 * e]), __uint_as_float(r[q * 8 + 2 * e + 1])),
                                                wt[q * 4 + e]);
                             a[e] = la_split(x);
                             b[e] = pack_bf16x2(x.x, x.y);
@@ -921,14 +913,24 @@ __global__ void __launch_bounds__(256) linattn_segments_kernel(LaPass p, float* 
     const float g = la_clamp_decay(p.log_decay[h]);
     float* a = seg + (size_t)item * nseg * dd + e;
     if (p.h0) a[(size_t)(nseg - 1) * dd] = p.h0[(size_t)item * dd + e];
+    // whole segments share a decay; eight states are on their way at once
+    const float2 whole = la_decay_pair_of(g, (float)(seg_chunks * kLaTok));
     float s = a[0];
-    for (int i = 1; i < nseg - 1; ++i) {
-        const int c0 = min(i * seg_chunks, nch), c1 = min(c0 + seg_chunks, nch);
-        const int tok = (c1 - c0) * kLaTok - (ragged >= c0 && ragged < c1 ? missing : 0);
-        float hi, lo;
-        la_decay_pair(g, (float)tok, hi, lo);
-        s = fmaf(s, hi, fmaf(s, lo, a[(size_t)i * dd]));
-        a[(size_t)i * dd] = s;
+    for (int i0 = 1; i0 < nseg - 1; i0 += 8) {
+        float x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x[u] = i0 + u < nseg - 1 ? a[(size_t)(i0 + u) * dd] : 0.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u;
+            if (i >= nseg - 1) break;
+            const int c0 = min(i * seg_chunks, nch), c1 = min(c0 + seg_chunks, nch);
+            const int tok = (c1 - c0) * kLaTok - (ragged >= c0 && ragged < c1 ? missing : 0);
+            float2 e = whole;
+            if (tok != seg_chunks * kLaTok) la_decay_pair(g, (float)tok, e.x, e.y);
+            s = fmaf(s, e.x, fmaf(s, e.y, x[u]));
+            a[(size_t)i * dd] = s;
+        }
     }
 }
 

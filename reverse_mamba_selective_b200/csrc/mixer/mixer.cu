@@ -381,7 +381,7 @@ r2l_status r2l_qk_norm_rope_bwd(const r2l_qk_norm_rope_args* a, const void* dq_o
     }
     if (!want_w) return R2L_OK;
     // sums over nothing are zero: n is 0 then and the partials are not read
-    return cuda_ok(launch_pdl(qk_norm_rope_dw_kernel, dim3((a->head_dim + 31) / 32, 2), dim3(256), 0, stream,
+    return cuda_ok(launch_pdl(qk_norm_rope_dw_kernel, dim3((a->head_dim + 31) / 32, 2), dim3(kRopeDwThreads), 0, stream,
                               static_cast<const float*>(workspace), n, a->head_dim, dq_weight, dk_weight),
                    "weight gradient sum launch")
                ? R2L_OK

@@ -7,13 +7,17 @@
 // shuffle tree, and the token's angles and the weights stay in registers.  (Angles and weights in shared memory, read
 // anew for every head, bound the kernel at 3.9 TB/s by bank conflicts.)  The heads ahead are on their way into a ring of
 // shared memory that every lane has to itself, with no barrier: registers for them left too few bytes in flight
-// (4.1 TB/s).  Angles are formed in fp64 up to the
+// (4.1 TB/s).  What was left was bound by what it issued (74 % of the slots): paired fp32 operations and addresses
+// formed once a token took 32768 tokens of 24 heads of 128 from 81 to 72 us (5.6 TB/s), and the gradients of 16384 tokens
+// from 66 to 64 us (4.8 TB/s; their two operands and the sums of dw take all registers of two CTAs an SM).  64 tokens
+// take 4 us, a launch and one trip through memory.  Angles are formed in fp64 up to the
 // fraction of a turn: position 100000 x frequency 1 leaves fp32 half a degree.
 #pragma once
 
 #include <algorithm>
 
 #include "../common.cuh"
+#include "pairs.cuh"
 
 namespace r2l {
 
@@ -42,16 +46,16 @@ template <typename T, int V, int N, int P>
 struct RopeRing {
     uint4* mine;  // [N][P][kRopeThreads], this lane's column
     __device__ __forceinline__ RopeRing(uint4* ring) : mine(ring + threadIdx.x) {}
-    // src NULL: zeros
-    __device__ __forceinline__ void fetch(int slot, int piece, const T* src, const T* any) {
+    // zeros unless `in`, and then src is not read
+    __device__ __forceinline__ void fetch(int slot, int piece, const T* src, bool in) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(mine + (slot * P + piece) * kRopeThreads)),
-                     "l"(src ? src : any), "r"(src ? 16 : 0)
+                     "l"(src), "r"(in ? 16 : 0)
                      : "memory");
     }
     __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
     // until at most N - 1 heads are on their way
     __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N - 1) : "memory"); }
-    __device__ __forceinline__ void get(int slot, int piece, const T*, float (&f)[V]) {
+    __device__ __forceinline__ void get(int slot, int piece, const T*, bool, float (&f)[V]) {
         const uint4 v = *(mine + (slot * P + piece) * kRopeThreads);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -68,10 +72,10 @@ struct RopeRing {
 template <typename T, int N, int P>
 struct RopeRing<T, 1, N, P> {
     __device__ __forceinline__ RopeRing(uint4*) {}
-    __device__ __forceinline__ void fetch(int, int, const T*, const T*) {}
+    __device__ __forceinline__ void fetch(int, int, const T*, bool) {}
     __device__ __forceinline__ void commit() {}
     __device__ __forceinline__ void wait() {}
-    __device__ __forceinline__ void get(int, int, const T* src, float (&f)[1]) { f[0] = src ? to_f32(*src) : 0.f; }
+    __device__ __forceinline__ void get(int, int, const T* src, bool in, float (&f)[1]) { f[0] = in ? to_f32(*src) : 0.f; }
 };
 template <int V>
 constexpr int rope_ring_bytes(int n, int p) {
@@ -110,9 +114,9 @@ __device__ __forceinline__ void rope_slot(int s, int dim, int rot, bool inter, i
     if (b >= np) b = -1;
 }
 
-// The slot's angles: (cos, sin) for the pair i of its channels, (1, 0) where it does not rotate.
+// The slot's angles: cos and sin (times sign) for the pair i of its channels, 1 and 0 where it does not rotate.
 template <int V>
-__device__ __forceinline__ void rope_angles(const RopeParams& p, int token, int a, int b, float2 (&cs)[V]) {
+__device__ __forceinline__ void rope_angles(const RopeParams& p, int token, int a, int b, float sign, float (&co)[V], float (&si)[V]) {
     const bool inter = p.interleaved != 0;
     const double pos = p.rot == 0 ? 0.0
                        : p.pos64  ? (double)static_cast<const long long*>(p.positions)[token]
@@ -128,28 +132,41 @@ __device__ __forceinline__ void rope_angles(const RopeParams& p, int token, int 
             f = a * V < p.rot ? a * V / 2 + i : -1;
         else
             f = b * V < p.rot ? b * V / 2 + i - V / 2 : -1;
-        cs[i] = make_float2(1.f, 0.f);
+        co[i] = 1.f, si[i] = 0.f;
         if (a >= 0 && f >= 0) {
             const double turns = pos * (double)__ldg(p.inv_freq + f) * 0.15915494309189535;  // 1 / (2 pi)
-            sincospif((float)(2.0 * (turns - rint(turns))), &cs[i].y, &cs[i].x);
+            sincospif((float)(2.0 * (turns - rint(turns))), &si[i], &co[i]);
+            si[i] *= sign;
         }
     }
 }
 
-// Rotates the slot's channels; sign -1 takes the rotation back.
 template <int V>
-__device__ __forceinline__ void rope_rotate(float (&xa)[V], float (&xb)[V], int a, int b, int rot, bool inter, float sign,
-                                            const float2 (&cs)[V]) {
-    if (!inter || V == 1) {
-        if (a >= 0 && (inter ? a < rot : a < rot / 2 / V)) {
+__device__ __forceinline__ float2 rope_pair(const float (&x)[V], int i) {
+    return make_float2(x[i], x[i + 1]);
+}
+
+// Rotates the slot's channels.
+template <int V>
+__device__ __forceinline__ void rope_rotate(float (&xa)[V], float (&xb)[V], int a, int b, int rot, bool inter, const float (&co)[V],
+                                            const float (&si)[V]) {
+    if constexpr (V == 1) {
+        if (a >= 0 && (inter ? a < rot : a < rot / 2)) {
+            const float u = xa[0], w = xb[0];
+            xa[0] = u * co[0] - w * si[0];
+            xb[0] = w * co[0] + u * si[0];
+        }
+    } else if (!inter) {
+        if (a >= 0 && a < rot / 2 / V) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float sn = sign * cs[i].y, u = xa[i], w = xb[i];
-                xa[i] = u * cs[i].x - w * sn;
-                xb[i] = w * cs[i].x + u * sn;
+            for (int i = 0; i < V; i += 2) {
+                const float2 u = rope_pair(xa, i), w = rope_pair(xb, i), c = rope_pair(co, i), s = rope_pair(si, i);
+                const float2 x = fma2(u, c, mul2(w, make_float2(-s.x, -s.y))), y = fma2(w, c, mul2(u, s));
+                xa[i] = x.x, xa[i + 1] = x.y;
+                xb[i] = y.x, xb[i + 1] = y.y;
             }
         }
-    } else if constexpr (V > 1) {
+    } else {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float(&x)[V] = half ? xb : xa;
@@ -157,12 +174,78 @@ __device__ __forceinline__ void rope_rotate(float (&xa)[V], float (&xb)[V], int 
             if (piece >= 0 && piece * V < rot) {
 #pragma unroll
                 for (int i = 0; i < V; i += 2) {
-                    const float2 t = cs[half * (V / 2) + i / 2];
-                    const float sn = sign * t.y, u = x[i], w = x[i + 1];
-                    x[i] = u * t.x - w * sn;
-                    x[i + 1] = w * t.x + u * sn;
+                    const float c = co[half * (V / 2) + i / 2], sn = si[half * (V / 2) + i / 2], u = x[i], w = x[i + 1];
+                    x[i] = u * c - w * sn;
+                    x[i + 1] = w * c + u * sn;
                 }
             }
+        }
+    }
+}
+
+// s += the sum of a b, in two halves where V allows.
+template <int V>
+__device__ __forceinline__ void rope_dot(float2& s, const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 1) {
+        s.x = fmaf(a[0], b[0], s.x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) s = fma2(rope_pair(a, i), rope_pair(b, i), s);
+    }
+}
+
+// y = a b
+template <int V>
+__device__ __forceinline__ void rope_times(float (&y)[V], const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 1) {
+        y[0] = a[0] * b[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float2 t = mul2(rope_pair(a, i), rope_pair(b, i));
+            y[i] = t.x, y[i + 1] = t.y;
+        }
+    }
+}
+
+// y = (s a) b
+template <int V>
+__device__ __forceinline__ void rope_mul(float (&y)[V], float s, const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 1) {
+        y[0] = s * a[0] * b[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float2 t = mul2(mul2(make_float2(s, s), rope_pair(a, i)), rope_pair(b, i));
+            y[i] = t.x, y[i + 1] = t.y;
+        }
+    }
+}
+
+// y += s a
+template <int V>
+__device__ __forceinline__ void rope_axpy(float (&y)[V], float s, const float (&a)[V]) {
+    if constexpr (V == 1) {
+        y[0] = fmaf(s, a[0], y[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float2 t = fma2(make_float2(s, s), rope_pair(a, i), rope_pair(y, i));
+            y[i] = t.x, y[i + 1] = t.y;
+        }
+    }
+}
+
+// y += (s a) b
+template <int V>
+__device__ __forceinline__ void rope_fma(float (&y)[V], float s, const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 1) {
+        y[0] = fmaf(s * a[0], b[0], y[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float2 t = fma2(mul2(make_float2(s, s), rope_pair(a, i)), rope_pair(b, i), rope_pair(y, i));
+            y[i] = t.x, y[i + 1] = t.y;
         }
     }
 }
@@ -213,44 +296,50 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_kernel(const __g
 
     extern __shared__ __align__(16) uint4 rope_ring[];
     RopeRing<T, V, U, 2> ring(rope_ring);
-    // head i of the group and its slot's pieces (NULL: none)
-    auto source = [&](int i, int piece) -> const T* {
-        const int hh = h0 + i, w = hh >= p.heads[0];
-        if (i >= hn || piece < 0) return nullptr;
-        return static_cast<const T*>(p.x[w]) + (size_t)token * p.x_tok[w] + (size_t)(w ? hh - p.heads[0] : hh) * p.dim + piece * V;
-    };
-    const T* any = static_cast<const T*>(p.heads[0] > 0 ? p.x[0] : p.x[1]);
+    // a token's heads, numbered through: queries, then keys (whose pointers count from the first query on)
+    const T* xs[2];
+    T* outs[2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        ring.fetch(u, 0, source(u, pa[0]), any);
-        ring.fetch(u, 1, source(u, pb[0]), any);
-        ring.commit();
+    for (int w = 0; w < 2; ++w) {
+        const long long from = w ? -(long long)p.heads[0] * p.dim : 0;
+        xs[w] = static_cast<const T*>(p.x[w]) + ((long long)token * p.x_tok[w] + from);
+        outs[w] = static_cast<T*>(p.out[w]) + ((long long)token * p.out_tok[w] + from);
     }
-    float2 cs[SL][V];
+    // head i of the group; behind the last one the token's first, which is not read there
+    auto source = [&](int i) -> const T* {
+        const int hh = i < hn ? h0 + i : 0;
+        return (hh >= p.heads[0] ? xs[1] : xs[0]) + (long long)hh * p.dim;
+    };
+    auto fetch = [&](int slot, int i) {
+        const T* x = source(i);
+        ring.fetch(slot, 0, x + max(pa[0], 0) * V, i < hn && pa[0] >= 0);
+        ring.fetch(slot, 1, x + max(pb[0], 0) * V, i < hn && pb[0] >= 0);
+        ring.commit();
+    };
 #pragma unroll
-    for (int j = 0; j < SL; ++j) rope_angles<V>(p, token, pa[j], pb[j], cs[j]);
+    for (int u = 0; u < U; ++u) fetch(u, u);
+    float co[SL][V], si[SL][V];
+#pragma unroll
+    for (int j = 0; j < SL; ++j) rope_angles<V>(p, token, pa[j], pb[j], 1.f, co[j], si[j]);
     float wa[SL][V], wb[SL][V];
     int wcur = -1;
     // the same count in the whole warp: the shuffles need all lanes
     int slot = 0;
     for (int i = 0; i < per; ++i) {
         const int hh = h0 + i, w = hh >= p.heads[0];
-        float ya[SL][V], yb[SL][V], ss = 0.f;
+        float ya[SL][V], yb[SL][V];
+        float2 ss = make_float2(0.f, 0.f);
         ring.wait();
+        const T* x = V > 1 ? nullptr : source(i);
 #pragma unroll
         for (int j = 0; j < SL; ++j) {
-            ring.get(slot, 0, source(i, pa[j]), ya[j]);
-            ring.get(slot, 1, source(i, pb[j]), yb[j]);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                ss = fmaf(ya[j][e], ya[j][e], ss);
-                ss = fmaf(yb[j][e], yb[j][e], ss);
-            }
+            ring.get(slot, 0, x + pa[j] * V, i < hn && pa[j] >= 0, ya[j]);
+            ring.get(slot, 1, x + pb[j] * V, i < hn && pb[j] >= 0, yb[j]);
+            rope_dot<V>(ss, ya[j], ya[j]);
+            rope_dot<V>(ss, yb[j], yb[j]);
         }
-        const float inv = rsqrtf(fmaf(rope_group_sum<G>(ss), p.inv_dim, p.eps));
-        ring.fetch(slot, 0, source(i + U, pa[0]), any);
-        ring.fetch(slot, 1, source(i + U, pb[0]), any);
-        ring.commit();
+        const float inv = rsqrtf(fmaf(rope_group_sum<G>(ss.x + ss.y), p.inv_dim, p.eps));
+        fetch(slot, i + U);
         slot = slot + 1 == U ? 0 : slot + 1;
         if (i >= hn) continue;
         if (w != wcur) {
@@ -261,15 +350,12 @@ __global__ void __launch_bounds__(kRopeThreads, 3) qk_norm_rope_kernel(const __g
                 rope_weight<V>(p, w, pb[j], wb[j]);
             }
         }
-        T* out = static_cast<T*>(p.out[w]) + (size_t)token * p.out_tok[w] + (size_t)(w ? hh - p.heads[0] : hh) * p.dim;
+        T* out = (w ? outs[1] : outs[0]) + (long long)hh * p.dim;
 #pragma unroll
         for (int j = 0; j < SL; ++j) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                ya[j][e] *= inv * wa[j][e];
-                yb[j][e] *= inv * wb[j][e];
-            }
-            rope_rotate<V>(ya[j], yb[j], pa[j], pb[j], p.rot, inter, 1.f, cs[j]);
+            rope_mul<V>(ya[j], inv, wa[j], ya[j]);
+            rope_mul<V>(yb[j], inv, wb[j], yb[j]);
+            rope_rotate<V>(ya[j], yb[j], pa[j], pb[j], p.rot, inter, co[j], si[j]);
             if (pa[j] >= 0) rope_store<T, V>(out + pa[j] * V, ya[j]);
             if (pb[j] >= 0) rope_store<T, V>(out + pb[j] * V, yb[j]);
         }
@@ -307,56 +393,57 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const
         const T* x = static_cast<const T*>(p.x[w]) + (size_t)token * p.x_tok[w];
         const T* dy = static_cast<const T*>(p.dy[w]) + (size_t)token * p.dy_tok[w];
         T* out = static_cast<T*>(p.out[w]) + (size_t)token * p.out_tok[w];
-        auto source = [&](const T* from, int h, int piece) -> const T* {
-            return live && h < heads && piece >= 0 ? from + (size_t)h * p.dim + piece * V : nullptr;
-        };
+        // behind the last head the first, which is not read there
         auto fetch = [&](int slot, int h) {
-            ring.fetch(slot, 0, source(x, h, pa[0]), x);
-            ring.fetch(slot, 1, source(x, h, pb[0]), x);
-            ring.fetch(slot, 2, source(dy, h, pa[0]), x);
-            ring.fetch(slot, 3, source(dy, h, pb[0]), x);
+            const bool in = live && h < heads;
+            const long long at = in ? (long long)h * p.dim : 0;
+            ring.fetch(slot, 0, x + at + max(pa[0], 0) * V, in && pa[0] >= 0);
+            ring.fetch(slot, 1, x + at + max(pb[0], 0) * V, in && pb[0] >= 0);
+            ring.fetch(slot, 2, dy + at + max(pa[0], 0) * V, in && pa[0] >= 0);
+            ring.fetch(slot, 3, dy + at + max(pb[0], 0) * V, in && pb[0] >= 0);
             ring.commit();
         };
 #pragma unroll
         for (int u = 0; u < U; ++u) fetch(u, u);
-        float2 cs[SL][V];
+        float co[SL][V], si[SL][V];
 #pragma unroll
-        for (int j = 0; j < SL; ++j) rope_angles<V>(p, token, pa[j], pb[j], cs[j]);
+        for (int j = 0; j < SL; ++j) rope_angles<V>(p, token, pa[j], pb[j], -1.f, co[j], si[j]);
         int slot = 0;
         for (int h = 0; h < heads; ++h) {
             float xa[SL][V], xb[SL][V], ua[SL][V], ub[SL][V];
-            float ss = 0.f, dot = 0.f;
+            float2 ss = make_float2(0.f, 0.f), dot = ss;
             ring.wait();
+            const long long at = (long long)h * p.dim;
 #pragma unroll
             for (int j = 0; j < SL; ++j) {
-                ring.get(slot, 0, source(x, h, pa[j]), xa[j]);
-                ring.get(slot, 1, source(x, h, pb[j]), xb[j]);
-                ring.get(slot, 2, source(dy, h, pa[j]), ua[j]);
-                ring.get(slot, 3, source(dy, h, pb[j]), ub[j]);
-                rope_rotate<V>(ua[j], ub[j], pa[j], pb[j], p.rot, inter, -1.f, cs[j]);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    ss = fmaf(xa[j][i], xa[j][i], ss);
-                    ss = fmaf(xb[j][i], xb[j][i], ss);
-                    dot = fmaf(ua[j][i] * wa[j][i], xa[j][i], dot);
-                    dot = fmaf(ub[j][i] * wb[j][i], xb[j][i], dot);
-                }
+                ring.get(slot, 0, x + at + pa[j] * V, live && pa[j] >= 0, xa[j]);
+                ring.get(slot, 1, x + at + pb[j] * V, live && pb[j] >= 0, xb[j]);
+                ring.get(slot, 2, dy + at + pa[j] * V, live && pa[j] >= 0, ua[j]);
+                ring.get(slot, 3, dy + at + pb[j] * V, live && pb[j] >= 0, ub[j]);
+                rope_rotate<V>(ua[j], ub[j], pa[j], pb[j], p.rot, inter, co[j], si[j]);
+                rope_dot<V>(ss, xa[j], xa[j]);
+                rope_dot<V>(ss, xb[j], xb[j]);
+                float t[V];
+                rope_times<V>(t, ua[j], wa[j]);
+                rope_dot<V>(dot, t, xa[j]);
+                rope_times<V>(t, ub[j], wb[j]);
+                rope_dot<V>(dot, t, xb[j]);
             }
-            const float inv = rsqrtf(fmaf(rope_group_sum<G>(ss), p.inv_dim, p.eps));
-            const float m = rope_group_sum<G>(dot) * p.inv_dim * inv * inv;  // mean(u w z) / rms
+            const float inv = rsqrtf(fmaf(rope_group_sum<G>(ss.x + ss.y), p.inv_dim, p.eps));
+            const float m = rope_group_sum<G>(dot.x + dot.y) * p.inv_dim * inv * inv;  // mean(u w z) / rms
             fetch(slot, h + U);
             slot = slot + 1 == U ? 0 : slot + 1;
             if (!live) continue;
 #pragma unroll
             for (int j = 0; j < SL; ++j) {
                 float oa[V], ob[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    da[j][i] = fmaf(ua[j][i], xa[j][i] * inv, da[j][i]);
-                    db[j][i] = fmaf(ub[j][i], xb[j][i] * inv, db[j][i]);
-                    oa[i] = inv * (ua[j][i] * wa[j][i] - xa[j][i] * m);
-                    ob[i] = inv * (ub[j][i] * wb[j][i] - xb[j][i] * m);
-                }
+                rope_fma<V>(da[j], inv, xa[j], ua[j]);
+                rope_fma<V>(db[j], inv, xb[j], ub[j]);
+                // inv (u w - x m)
+                rope_mul<V>(oa, inv, ua[j], wa[j]);
+                rope_axpy<V>(oa, -inv * m, xa[j]);
+                rope_mul<V>(ob, inv, ub[j], wb[j]);
+                rope_axpy<V>(ob, -inv * m, xb[j]);
                 if (pa[j] >= 0) rope_store<T, V>(out + (size_t)h * p.dim + pa[j] * V, oa);
                 if (pb[j] >= 0) rope_store<T, V>(out + (size_t)h * p.dim + pb[j] * V, ob);
             }
@@ -383,22 +470,24 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const
     }
 }
 
-// dw[c] = sum over the `n` CTAs' partials, 8 warps a CTA, each a fixed share, 32 channels a CTA.
-__global__ void __launch_bounds__(256)
+// dw[c] = sum over the `n` CTAs' partials, 32 warps a CTA, each a fixed share, 32 channels a CTA.
+constexpr int kRopeDwThreads = 1024;
+__global__ void __launch_bounds__(kRopeDwThreads)
     qk_norm_rope_dw_kernel(const float* __restrict__ part, int n, int dim, float* dq_weight, float* dk_weight) {
-    __shared__ float red[8][32];
+    __shared__ float red[32][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = blockIdx.x * 32 + lane, w = blockIdx.y;
     pdl_trigger();
     pdl_wait();
     float s = 0.f;
     if (c < dim)
-        for (int i = warp; i < n; i += 8) s += part[((size_t)w * n + i) * dim + c];
+#pragma unroll 5
+        for (int i = warp; i < n; i += 32) s += part[((size_t)w * n + i) * dim + c];
     red[warp][lane] = s;
     __syncthreads();
     float* out = w ? dk_weight : dq_weight;
     if (warp == 0 && c < dim && out) {
-        for (int i = 1; i < 8; ++i) s += red[i][lane];
+        for (int i = 1; i < 32; ++i) s += red[i][lane];
         out[c] = s;
     }
 }
