@@ -30,7 +30,7 @@
 // against 149), a truncating split (172 against 169).
 //
 // The pass over the states of a divided sequence (Y false) has room for two K~ and two KV: the next chunk's K~ is
-// made before this one's KV is waited for, 1.6 us a chunk instead of 2.0.
+// made before this one's KV is waited for (one sequence of 32768 tokens of 16 heads: 248 -> 226 us in all, now 221).
 //
 // Masked places never reach an output: rows of V past a sequence's length are zeroed, keys past it are not read into
 // K~, and where an output comes out not finite (a masked weight is a zero factor, and zero times an infinity is
