@@ -9,7 +9,7 @@
 // shared memory that every lane has to itself, with no barrier: registers for them left too few bytes in flight
 // (4.1 TB/s).  What was left was bound by what it issued (74 % of the slots): paired fp32 operations and addresses
 // formed once a token took 32768 tokens of 24 heads of 128 from 81 to 72 us (5.6 TB/s), and the gradients of 16384 tokens
-// from 66 to 64 us (4.8 TB/s; their two operands and the sums of dw take all registers of two CTAs an SM).  64 tokens
+// from 66 to 64 us; there the ring runs on across tokens, three heads ahead: 61 us (5.0 TB/s, two CTAs an SM).  64 tokens
 // take 4 us, a launch and one trip through memory.  Angles are formed in fp64 up to the
 // fraction of a turn: position 100000 x frequency 1 leaves fp32 half a degree.
 #pragma once
@@ -24,7 +24,7 @@ namespace r2l {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxDim = 256;
 constexpr int kRopeAhead = 4;     // heads that a group has in flight, forward
-constexpr int kRopeAheadBwd = 2;  // and in the gradients (two operands)
+constexpr int kRopeAheadBwd = 3;  // and in the gradients (two operands)
 
 struct RopeParams {
     const void *x[2], *dy[2];   // queries, keys
@@ -386,29 +386,37 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const
     extern __shared__ __align__(16) uint4 rope_ring[];
     constexpr int U = kRopeAheadBwd;
     RopeRing<T, V, U, 4> ring(rope_ring);
-    // a group walks over whole tokens, kGroups * gridDim.x apart (the same count in the whole CTA)
-    for (long long t0 = (long long)blockIdx.x * kGroups; t0 < p.tokens && heads > 0; t0 += (long long)gridDim.x * kGroups) {
+    // A group walks over whole tokens, kGroups * gridDim.x apart (the same count in the whole CTA); the ring runs on from a
+    // token's last head to the next one's first.
+    const long long step = (long long)gridDim.x * kGroups;
+    long long ft = (long long)blockIdx.x * kGroups + g;  // what is fetched next
+    int fh = 0;
+    auto fetch = [&](int slot) {
+        const bool in = ft < p.tokens;
+        const long long at = (long long)fh * p.dim, t = in ? ft : 0;
+        const T* x = static_cast<const T*>(p.x[w]) + (in ? t * p.x_tok[w] + at : 0);
+        const T* dy = static_cast<const T*>(p.dy[w]) + (in ? t * p.dy_tok[w] + at : 0);
+        ring.fetch(slot, 0, x + max(pa[0], 0) * V, in && pa[0] >= 0);
+        ring.fetch(slot, 1, x + max(pb[0], 0) * V, in && pb[0] >= 0);
+        ring.fetch(slot, 2, dy + max(pa[0], 0) * V, in && pa[0] >= 0);
+        ring.fetch(slot, 3, dy + max(pb[0], 0) * V, in && pb[0] >= 0);
+        ring.commit();
+        if (++fh == heads) fh = 0, ft += step;
+    };
+    if (heads > 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) fetch(u);
+    }
+    int slot = 0;
+    for (long long t0 = (long long)blockIdx.x * kGroups; t0 < p.tokens && heads > 0; t0 += step) {
         const bool live = t0 + g < p.tokens;
         const int token = live ? (int)(t0 + g) : 0;
         const T* x = static_cast<const T*>(p.x[w]) + (size_t)token * p.x_tok[w];
         const T* dy = static_cast<const T*>(p.dy[w]) + (size_t)token * p.dy_tok[w];
         T* out = static_cast<T*>(p.out[w]) + (size_t)token * p.out_tok[w];
-        // behind the last head the first, which is not read there
-        auto fetch = [&](int slot, int h) {
-            const bool in = live && h < heads;
-            const long long at = in ? (long long)h * p.dim : 0;
-            ring.fetch(slot, 0, x + at + max(pa[0], 0) * V, in && pa[0] >= 0);
-            ring.fetch(slot, 1, x + at + max(pb[0], 0) * V, in && pb[0] >= 0);
-            ring.fetch(slot, 2, dy + at + max(pa[0], 0) * V, in && pa[0] >= 0);
-            ring.fetch(slot, 3, dy + at + max(pb[0], 0) * V, in && pb[0] >= 0);
-            ring.commit();
-        };
-#pragma unroll
-        for (int u = 0; u < U; ++u) fetch(u, u);
         float co[SL][V], si[SL][V];
 #pragma unroll
         for (int j = 0; j < SL; ++j) rope_angles<V>(p, token, pa[j], pb[j], -1.f, co[j], si[j]);
-        int slot = 0;
         for (int h = 0; h < heads; ++h) {
             float xa[SL][V], xb[SL][V], ua[SL][V], ub[SL][V];
             float2 ss = make_float2(0.f, 0.f), dot = ss;
@@ -431,7 +439,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) qk_norm_rope_bwd_kernel(const
             }
             const float inv = rsqrtf(fmaf(rope_group_sum<G>(ss.x + ss.y), p.inv_dim, p.eps));
             const float m = rope_group_sum<G>(dot.x + dot.y) * p.inv_dim * inv * inv;  // mean(u w z) / rms
-            fetch(slot, h + U);
+            fetch(slot);
             slot = slot + 1 == U ? 0 : slot + 1;
             if (!live) continue;
 #pragma unroll
