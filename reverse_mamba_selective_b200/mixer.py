@@ -203,7 +203,9 @@ def _linattn_args(q, k, v, log_decay, scale, block_len, reverse, seq_lens, lead,
     d_k = q.shape[-1]
     if k.shape[-1] != d_k:
         raise ValueError("q and k must have the same head size")
-    if isinstance(log_decay, torch.Tensor) and log_decay.dim() != 1:
+    if not isinstance(log_decay, torch.Tensor):
+        raise TypeError("log_decay must be a CUDA tensor")
+    if log_decay.dim() != 1:
         raise ValueError("log_decay must have shape [heads]")
     decay = _ptr_of("log_decay", log_decay, torch.float32, None, index)
     lens = _ptr_of("seq_lens", seq_lens, torch.int32, (batch,), index)
@@ -339,6 +341,8 @@ def _rope_args(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, 
         rot = 2 * inv_freq.shape[0]
         if positions is None:
             raise ValueError("positions must be given with inv_freq")
+        if not isinstance(positions, torch.Tensor):
+            raise TypeError("positions must be a CUDA tensor")
         wide = 1 if positions.dtype is torch.int64 else 0
         if not wide and positions.dtype is not torch.int32:
             raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")

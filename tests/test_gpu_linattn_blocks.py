@@ -151,3 +151,53 @@ def test_two_calls_at_once(r2l):
     for i in range(2):
         for g in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
+def test_two_graphs_share_a_workspace(r2l):
+    """Captured calls that use one workspace (segments' states, shared heads' gradients), replayed in turn."""
+    cases = [make(5, 1, 3000, 2, 1, 1, 2, 64, 64, "bf16"), make(6, 2, 1500, 2, 2, 1, 2, 64, 64, "bf16")]
+    dys = [torch.randn(*c[2].shape[:2], c[3].shape[0], 64, generator=torch.Generator().manual_seed(7)).to(torch.bfloat16).to(DEV)
+           for c in cases]
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+
+    def run(c, dy, **kw):
+        y, h = r2l.r2l_linattn(*c, want_h_last=True, **kw)
+        g = r2l.r2l_linattn_bwd(*c, dy, **kw)
+        return [y, h, g["dq"], g["dk"], g["dv"]]
+
+    want = [run(c, dy) for c, dy in zip(cases, dys)]
+    graphs, got = [], []
+    for c, dy in zip(cases, dys):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(run(c, dy, workspace=ws))
+    for i in (0, 1, 0, 1):
+        graphs[i].replay()
+        assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
+    small = torch.empty(256, dtype=torch.uint8, device=DEV)
+    with pytest.raises(r2l.MixerError):
+        r2l.r2l_linattn(*cases[0], workspace=small)
+    del graphs
+
+
+def test_binding_refusals(r2l):
+    q, k, v, g = make(1, 2, 20, 4, 4, 2, 4, 64, 64, "bf16")
+    ok = lambda **kw: r2l.r2l_linattn(q, k, v, g, **kw)
+    for bad, err in ((lambda: r2l.r2l_linattn(q, k, v, None), TypeError), (lambda: r2l.r2l_linattn(q, k.float(), v, g), TypeError),
+                     (lambda: r2l.r2l_linattn(q.half(), k.half(), v.half(), g), TypeError),
+                     (lambda: r2l.r2l_linattn(q, k[..., :32], v, g), ValueError),
+                     (lambda: r2l.r2l_linattn(q, k, v.transpose(1, 2), g), ValueError),
+                     (lambda: r2l.r2l_linattn(q[:1].expand(2, -1, -1, -1), k, v, g), ValueError),
+                     (lambda: r2l.r2l_linattn(q, k, v, g[:3].contiguous()), r2l.MixerError),
+                     (lambda: r2l.r2l_linattn(q.cpu(), k, v, g), TypeError),
+                     (lambda: ok(h0=torch.zeros(2, 4, 64, 32, device=DEV)), ValueError),
+                     (lambda: ok(h0=torch.zeros(2, 4, 64, 64, device=DEV, dtype=torch.bfloat16)), TypeError),
+                     (lambda: ok(reverse=True, block_len=6), r2l.MixerError),
+                     (lambda: ok(reverse=True, block_len=10, want_h_last=True), r2l.MixerError),
+                     (lambda: ok(seq_lens=torch.zeros(2, dtype=torch.int64, device=DEV)), TypeError),
+                     (lambda: r2l.r2l_linattn_step(q[:, 0], k[:, 0], v[:, 0], g, None), ValueError),
+                     (lambda: r2l.r2l_linattn_bwd(q, k, v, g, None), ValueError),
+                     (lambda: r2l.r2l_qk_norm_rope(q[0], k[0], None, None, [1] * 20, torch.ones(32, device=DEV)), TypeError)):
+        with pytest.raises(err):
+            bad()
+    ok()

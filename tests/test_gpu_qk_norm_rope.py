@@ -184,3 +184,25 @@ def test_stream_and_graph(r2l):
         assert torch.equal(a, want[0]) and torch.equal(b, want[1])
         assert all(torch.equal(cg[n], wg[n]) for n in wg)
     del graph
+
+
+@pytest.mark.parametrize("n,d", [(40001, 16), (20011, 64), (10007, 20)])
+def test_several_tokens_a_group(r2l, n, d):
+    # more tokens than the gradient kernel has groups of lanes: each walks over several, the loads running on between them
+    check(r2l, n, 3, 1, d, d, "bf16", seed=n)
+
+
+def test_two_graphs_share_a_workspace(r2l):
+    """Two captured gradient calls with one workspace, replayed in turn, give the plain calls' bits."""
+    cases = [make(s, n, 4, 2, 64, 64, "bf16") for s, n in ((1, 700), (2, 300))]
+    want = [r2l.r2l_qk_norm_rope_bwd(*c) for c in cases]
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    graphs, got = [], []
+    for c in cases:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(r2l.r2l_qk_norm_rope_bwd(*c, workspace=ws))
+    for i in (0, 1, 0, 1):
+        graphs[i].replay()
+        assert all(torch.equal(got[i][m], want[i][m]) for m in want[i])
+    del graphs
