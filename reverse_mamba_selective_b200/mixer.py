@@ -125,7 +125,7 @@ _HERE = _Here()
 
 def _on_device(index: int):
     """The tensors' device made current: the library works on the current device."""
-    return _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
+    return _HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
 def _stream_of(stream, index: int, *made):
@@ -166,17 +166,18 @@ def _first(name: str, t, dims: int) -> int:
 def _heads(name: str, t: torch.Tensor, dtype, lead: Tuple[int, ...], index: int) -> int:
     """Checks a [*lead, heads, d] operand (heads and channels dense, tokens evenly spaced over lead) and returns its
     elements from token to token (0: dense)."""
+    shape = t.shape if isinstance(t, torch.Tensor) else ()
+    fits = len(shape) == len(lead) + 2 and shape[:-2] == lead
+    if fits and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        return 0
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != len(lead) + 2 or shape[:-2] != lead:
+    if not fits:
         raise ValueError(f"{name} must have shape [{', '.join(map(str, lead))}, heads, d], got {tuple(shape)}")
     if t.get_device() != index:
         raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
-    if t.is_contiguous():
-        return 0
     strides = t.stride()
     heads, d = shape[-2], shape[-1]
     if (d > 1 and strides[-1] != 1) or (heads > 1 and strides[-2] != d):
@@ -200,8 +201,10 @@ def _linattn_args(q, k, v, log_decay, scale, block_len, reverse, seq_lens, lead,
     dtype = q.dtype
     qs, ks, vs = _heads("q", q, dtype, lead, index), _heads("k", k, dtype, lead, index), _heads("v", v, dtype, lead, index)
     batch, seqlen = lead if len(lead) == 2 else (lead[0], 1)
-    d_k = q.shape[-1]
-    if k.shape[-1] != d_k:
+    q_heads, d_k = q.shape[-2:]
+    k_heads, k_dim = k.shape[-2:]
+    v_heads, d_v = v.shape[-2:]
+    if k_dim != d_k:
         raise ValueError("q and k must have the same head size")
     if not isinstance(log_decay, torch.Tensor):
         raise TypeError("log_decay must be a CUDA tensor")
@@ -211,9 +214,14 @@ def _linattn_args(q, k, v, log_decay, scale, block_len, reverse, seq_lens, lead,
     lens = _ptr_of("seq_lens", seq_lens, torch.int32, (batch,), index)
     if scale is None:
         scale = d_k ** -0.5 if d_k else 1.0
-    return LinattnArgs(batch, seqlen, seqlen if block_len is None else int(block_len), log_decay.shape[0], q.shape[-2],
-                       k.shape[-2], v.shape[-2], d_k, v.shape[-1], 1 if reverse else 0, _DTYPE_CODE[dtype], scale,
+    return LinattnArgs(batch, seqlen, seqlen if block_len is None else int(block_len), log_decay.shape[0], q_heads,
+                       k_heads, v_heads, d_k, d_v, 1 if reverse else 0, _DTYPE_CODE[dtype], scale,
                        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, decay, lens)
+
+
+def _dense(t: torch.Tensor, shape) -> torch.Tensor:
+    """An uninitialised dense tensor of t's type and device."""
+    return torch.empty_like(t) if t.shape == shape and t.is_contiguous() else t.new_empty(shape)
 
 
 def _workspace(given: Optional[torch.Tensor], need: int, like: torch.Tensor, index: int):
@@ -254,7 +262,7 @@ def r2l_linattn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: to
             h_last = made_h = q.new_empty(state, dtype=torch.float32)
             p1 = h_last.data_ptr()
         if y is None:
-            y = made_y = q.new_empty(shape)
+            y = made_y = _dense(v, shape)
             py = y.data_ptr()
         ws, made, nbytes = _workspace(workspace, lib.r2l_linattn_workspace_size(ref), q, index)
         st = lib.r2l_linattn(ref, p0, p1, py, ws, nbytes, _stream_of(stream, index, made_h, made_y, made))
@@ -282,7 +290,7 @@ def r2l_linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     with _on_device(index):
         made = None
         if y is None:
-            y = made = q.new_empty(shape)
+            y = made = _dense(v, shape)
             py = y.data_ptr()
         st = lib.r2l_linattn_step(ctypes.byref(a), p0, p1, py, _stream_of(stream, index, made))
     if st != R2L_OK:
@@ -313,7 +321,7 @@ def r2l_linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
         want_dh0 = h0 is not None
     ref = ctypes.byref(a)
     with _on_device(index):
-        dq, dk, dv = q.new_empty(q.shape), q.new_empty(k.shape), q.new_empty(v.shape)
+        dq, dk, dv = _dense(q, q.shape), _dense(k, k.shape), _dense(v, v.shape)
         dh0 = q.new_empty(state, dtype=torch.float32) if want_dh0 else None
         ws, made, nbytes = _workspace(workspace, lib.r2l_linattn_bwd_workspace_size(ref), q, index)
         st = lib.r2l_linattn_bwd(ref, pdy, p0, pdh, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dh0), ws, nbytes,
@@ -368,11 +376,11 @@ def r2l_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.
     made_q = made_k = None
     with _on_device(index):
         if q_out is None:
-            q_out = made_q = q.new_empty(q.shape)
+            q_out = made_q = _dense(q, q.shape)
         else:
             qs = _heads("q_out", q_out, q.dtype, (a.tokens,), index)
         if k_out is None:
-            k_out = made_k = q.new_empty(k.shape)
+            k_out = made_k = _dense(k, k.shape)
         else:
             ks = _heads("k_out", k_out, q.dtype, (a.tokens,), index)
         for name, o, t in (("q_out", q_out, q), ("k_out", k_out, k)):
@@ -401,7 +409,7 @@ def r2l_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[to
     pdk = _ptr_of("dk_out", dk_out, q.dtype, k.shape, index)
     ref = ctypes.byref(a)
     with _on_device(index):
-        dq, dk = q.new_empty(q.shape), q.new_empty(k.shape)
+        dq, dk = _dense(q, q.shape), _dense(k, k.shape)
         dqw, dkw = q.new_empty(a.head_dim, dtype=torch.float32), q.new_empty(a.head_dim, dtype=torch.float32)
         ws, made, nbytes = _workspace(workspace, lib.r2l_qk_norm_rope_bwd_workspace_size(ref), q, index)
         st = lib.r2l_qk_norm_rope_bwd(ref, pdq, pdk, dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), ws, nbytes,
