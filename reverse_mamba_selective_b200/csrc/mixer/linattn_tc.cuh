@@ -960,13 +960,15 @@ inline bool la_encode(CUtensorMap* out, const void* base, int d, int heads, int 
 
 // How a pass is divided: segments per sequence and chunks in each.  Few (sequence, head) pairs are divided into as many
 // segments as fill the SMs, of four chunks at least.  Dividing runs the state part of a chunk (half its time) twice and
-// adds two launches and the segments' states (about 20 us): n segments pay from (1 - 1.55 / n) nch chunk times (2 us) on.
-// 64 pairs, n = 2, 32 chunks: 75 us undivided, 86 divided, equal at 48; 16 pairs, n = 9, 512 chunks: 1030 and 226 us.
+// adds two launches and the segments' states, 14 us and 0.2 a pair: n segments pay where (1 - 1.55 / n) nch chunk times
+// (2 us) exceed that.  64 pairs, n = 2: 32 chunks 75 us undivided, 86 divided, 47 chunks 104 and 109; 32 pairs, n = 4,
+// 16 chunks 38 and 38; 8 pairs, n = 4, 16 chunks 37 and 33; 16 pairs, n = 9, 512 chunks 1030 and 221 us.  (One launch in
+// which the second part's CTA forms the state before it itself gained nothing: the state is what takes the time.)
 inline void la_segments(int nseq, int heads, int seq_len, int nsm, int& nseg, int& seg_chunks) {
     const long long items = (long long)nseq * heads;
     const int nch = (seq_len + kLaTok - 1) / kLaTok;
     nseg = items > 0 ? (int)std::min<long long>(nsm / items, nch / 4) : 1;
-    if (nseg < 2 || (20 * nseg - 31) * nch < 200 * nseg) nseg = 1;
+    if (nseg < 2 || (20 * nseg - 31LL) * nch < (140 + 2 * items) * nseg) nseg = 1;
     seg_chunks = (nch + nseg - 1) / nseg;
     nseg = seg_chunks > 0 ? (nch + seg_chunks - 1) / seg_chunks : 1;
 }
