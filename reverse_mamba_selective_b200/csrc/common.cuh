@@ -153,17 +153,19 @@ inline bool cuda_ok(cudaError_t e, const char* where) {
 
 // Host: raise a kernel's dynamic shared-memory limit when a launch needs more than 48 KiB.
 // The limit is raised to exactly what is asked (the opt-in maximum minus the kernel's static
-// shared memory bounds it) and remembered per kernel, so steady-state launches skip the call.
+// shared memory bounds it) and remembered per kernel and device, so steady-state launches skip the call.
 inline int prepare_kernel_smem(const void* fn, int smem_bytes) {
     static std::mutex mu;
     static const void* fns[256];
-    static int limits[256];
+    static int devs[256], limits[256];
     static int n = 0;
     if (smem_bytes <= 48 * 1024) return 0;
+    int dev = 0;
+    if (!cuda_ok(cudaGetDevice(&dev), "cudaGetDevice")) return -1;
     std::lock_guard<std::mutex> lock(mu);
     int slot = -1;
     for (int i = 0; i < n; ++i)
-        if (fns[i] == fn) slot = i;
+        if (fns[i] == fn && devs[i] == dev) slot = i;
     if (slot >= 0 && limits[slot] >= smem_bytes) return 0;
     if (!cuda_ok(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes),
                  "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)"))
@@ -171,6 +173,7 @@ inline int prepare_kernel_smem(const void* fn, int smem_bytes) {
     if (slot < 0 && n < 256) {
         slot = n++;
         fns[slot] = fn;
+        devs[slot] = dev;
     }
     if (slot >= 0) limits[slot] = smem_bytes;
     return 0;
