@@ -14,6 +14,8 @@
 
 namespace r2l {
 
+constexpr int kLaTok = 64;        // tokens per chunk
+
 struct LaPass {
     const void *q, *k, *v;
     void* y;
@@ -61,6 +63,53 @@ __device__ __forceinline__ int la_len(const LaPass& p, int seq) {
     if (!p.lens) return p.seq_len;
     const int n = p.lens[seq];
     return n < 0 ? 0 : (n > p.seq_len ? p.seq_len : n);
+}
+
+// Up to three passes in one launch (the gradients): blockIdx.z says which.  nseg > 1: sequences are divided into segments of
+// seg_tok tokens, first their states alone (states), then, from those before each, the outputs.
+struct LaPasses {
+    LaPass p[3];
+    float* seg[3];  // [item][nseg] states after the segments but the last, then h0's copy
+    int nseg, seg_tok, states;
+};
+
+// States before the segments: seg[s] = gamma^tokens(s) seg[s - 1] + seg[s], in place (seg[0] is complete: its run
+// began with h0); and h0's copy, as it is stored, in the last place.
+__global__ void __launch_bounds__(256) linattn_segments_kernel(const __grid_constant__ LaPasses passes) {
+    const LaPass& p = passes.p[blockIdx.z];
+    const int nseg = passes.nseg, seg_chunks = passes.seg_tok / kLaTok;
+    pdl_trigger();
+    pdl_wait();
+    const int dd = p.dk * p.dv;
+    const int e = blockIdx.x * 256 + threadIdx.x;
+    const int item = blockIdx.y;
+    if (e >= dd) return;
+    const int seq = item / p.heads, h = item - seq * p.heads;
+    const int len = la_len(p, seq), nch = (len + kLaTok - 1) / kLaTok;
+    const int missing = nch * kLaTok - len;  // tokens that the ragged chunk lacks
+    const int ragged = p.reverse ? 0 : nch - 1;
+    const float g = la_clamp_decay(p.log_decay[h]);
+    float* a = passes.seg[blockIdx.z] + (size_t)item * nseg * dd + e;
+    if (p.h0) a[(size_t)(nseg - 1) * dd] = p.h0[(size_t)item * dd + e];
+    // whole segments share a decay; eight states are on their way at once
+    const float2 whole = la_decay_pair_of(g, (float)(seg_chunks * kLaTok));
+    float s = a[0];
+    for (int i0 = 1; i0 < nseg - 1; i0 += 8) {
+        float x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x[u] = i0 + u < nseg - 1 ? a[(size_t)(i0 + u) * dd] : 0.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u;
+            if (i >= nseg - 1) break;
+            const int c0 = min(i * seg_chunks, nch), c1 = min(c0 + seg_chunks, nch);
+            const int tok = (c1 - c0) * kLaTok - (ragged >= c0 && ragged < c1 ? missing : 0);
+            float2 e = whole;
+            if (tok != seg_chunks * kLaTok) la_decay_pair(g, (float)tok, e.x, e.y);
+            s = fmaf(s, e.x, fmaf(s, e.y, x[u]));
+            a[(size_t)i * dd] = s;
+        }
+    }
 }
 
 }  // namespace r2l

@@ -8,8 +8,8 @@
 // barriers), while the next tokens are on their way into registers.
 //
 // Runs in fp32 are bound by the FMA pipe where (sequence, head) pairs fill the GPU (4 operations an element and token),
-// else by the latency of a token; then the columns are spread over more CTAs, and the instructions of four tokens run
-// into each other.  Gradients of 2 x 8 sequences and heads of 200 tokens, 64 x 48: 44 us, 0.2 us a token of one pass (61 us
+// else by the latency of a token; then the columns are spread over more CTAs, the instructions of four tokens run
+// into each other, and long sequences are divided.  Gradients of 2 x 8 sequences and heads of 200 tokens, 64 x 48: 44 us, 0.2 us a token of one pass (61 us
 // a token at a time).  The step is bound by memory: 2048 states of 128 x 128, 44 us in and out, 6.1 TB/s.
 #pragma once
 
@@ -24,11 +24,6 @@ namespace r2l {
 constexpr int kRecThreads = 256;
 constexpr int kRecTok = 8;       // tokens staged at once: one a warp
 constexpr int kRecMaxD = 128;
-
-// Up to three passes in one launch (the gradients): blockIdx.z says which.
-struct LaPasses {
-    LaPass p[3];
-};
 
 // DK: 64 or 128, the passes' key channels at most.
 template <int TPR, int DK>
@@ -49,26 +44,48 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_c
     pdl_trigger();
     pdl_wait();
 
-    const long long item = blockIdx.x;
+    const bool quiet = passes.states != 0;
+    const int runs = passes.nseg - (quiet ? 1 : 0);
+    const long long item = blockIdx.x / (unsigned)runs;
+    const int sg = (int)(blockIdx.x - (unsigned)item * (unsigned)runs);
     const int seq = (int)(item / p.heads), h = (int)(item - (long long)seq * p.heads);
-    const int len = la_len(p, seq);
+    // this segment's tokens: `len` from the scan position `first` of the row's `all`
+    const int all = la_len(p, seq), first = (int)min((long long)sg * passes.seg_tok, (long long)all), len = min(all - first, passes.seg_tok);
+    const int t0 = p.reverse ? all - 1 - first : first, dt = p.reverse ? -1 : 1;
     const size_t tok0 = (size_t)seq * p.seq_len;
     const float* q = static_cast<const float*>(p.q) + tok0 * p.q_tok + (size_t)(h / p.q_div) * p.dk;
     const float* k = static_cast<const float*>(p.k) + tok0 * p.k_tok + (size_t)(h / p.k_div) * p.dk;
     const float* v = static_cast<const float*>(p.v) + tok0 * p.v_tok + (size_t)(h / p.v_div) * p.dv + c0;
     float* y = static_cast<float*>(p.y) + tok0 * p.y_tok + (size_t)h * p.dv + c0;
 
-    const size_t sbase = (size_t)item * p.dk * p.dv;
+    const size_t dd = (size_t)p.dk * p.dv, sbase = (size_t)item * dd;
+    float* const segs = passes.seg[blockIdx.z] + (size_t)item * passes.nseg * dd;
+    const float* in = nullptr;
+    float* out = nullptr;
+    bool in_t = p.h_t != 0, out_t = in_t;
+    if (sg == 0) {
+        // a divided sequence starts from the copy: its last segment may write h_last over h0 at any time
+        if (p.h0) in = passes.nseg > 1 && !quiet ? segs + (size_t)(passes.nseg - 1) * dd : p.h0 + sbase;
+    } else if (!quiet) {
+        in = segs + (size_t)(sg - 1) * dd;
+        in_t = false;
+    }
+    if (quiet) {
+        out = segs + (size_t)sg * dd;
+        out_t = false;
+    } else if (sg == passes.nseg - 1 && p.h_last) {
+        out = p.h_last + sbase;
+    }
     float4 s[M];
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         const int r = rr + m * ROWS;
         s[m] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.h0 && col_ok && r < p.dk) {
-            if (!p.h_t) {
-                s[m] = *reinterpret_cast<const float4*>(p.h0 + sbase + (size_t)r * p.dv + c0 + cq);
+        if (in && col_ok && r < p.dk) {
+            if (!in_t) {
+                s[m] = *reinterpret_cast<const float4*>(in + (size_t)r * p.dv + c0 + cq);
             } else {
-                const float* a = p.h0 + sbase + (size_t)(c0 + cq) * p.dk + r;
+                const float* a = in + (size_t)(c0 + cq) * p.dk + r;
                 s[m] = make_float4(a[0], a[p.dk], a[2 * p.dk], a[3 * p.dk]);
             }
         }
@@ -76,7 +93,7 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_c
     // the values of this warp's token of the group that begins at n0 (zeros past the end)
     float fq[J], fk[J], fv[JV];
     auto fetch = [&](int n0) {
-        const int n = n0 + warp, t = p.reverse ? len - 1 - n : n;
+        const int n = n0 + warp, t = t0 + dt * n;
         const bool live = n < len;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
@@ -103,8 +120,8 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_c
             if (lane + 32 * j < COLS) sv[warp][lane + 32 * j] = fv[j];
         __syncthreads();
         fetch(n0 + kRecTok);
-        auto tokens = [&](auto shift) {
-            constexpr bool SHIFT = decltype(shift)::value;
+        auto tokens = [&](auto shift, auto silent) {
+            constexpr bool SHIFT = decltype(shift)::value, QUIET = decltype(silent)::value;
 #pragma unroll U
             for (int tt = 0; tt < nt; ++tt) {
                 const float4 vv = *reinterpret_cast<const float4*>(&sv[tt][cq]);
@@ -121,10 +138,12 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_c
                         a.z = fmaf(a.z, ghi, fmaf(a.z, glo, qk.y * vv.z));
                         a.w = fmaf(a.w, ghi, fmaf(a.w, glo, qk.y * vv.w));
                     }
-                    o.x = fmaf(qk.x, a.x, o.x);
-                    o.y = fmaf(qk.x, a.y, o.y);
-                    o.z = fmaf(qk.x, a.z, o.z);
-                    o.w = fmaf(qk.x, a.w, o.w);
+                    if constexpr (!QUIET) {
+                        o.x = fmaf(qk.x, a.x, o.x);
+                        o.y = fmaf(qk.x, a.y, o.y);
+                        o.z = fmaf(qk.x, a.z, o.z);
+                        o.w = fmaf(qk.x, a.w, o.w);
+                    }
                     if constexpr (SHIFT) {
                         a.x = fmaf(a.x, ghi, a.x * glo);
                         a.y = fmaf(a.y, ghi, a.y * glo);
@@ -134,7 +153,8 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_c
                     s[m] = a;
                 }
                 // the warp's W rows: each step halves what a lane sums, down to one column a lane
-                if constexpr (W == 1) {
+                if constexpr (QUIET) {
+                } else if constexpr (W == 1) {
                     *reinterpret_cast<float4*>(&part[tt][warp][cq]) = o;
                 } else {
                     const bool hi = lane & TPR;
@@ -154,35 +174,42 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_c
                 }
             }
         };
-        if (p.shift)
-            tokens(std::true_type());
-        else
-            tokens(std::false_type());
+        if (quiet) {
+            if (p.shift)
+                tokens(std::true_type(), std::true_type());
+            else
+                tokens(std::false_type(), std::true_type());
+        } else if (p.shift) {
+            tokens(std::true_type(), std::false_type());
+        } else {
+            tokens(std::false_type(), std::false_type());
+        }
         __syncthreads();
+        if (quiet) continue;
         for (int i = tid; i < nt * COLS; i += kRecThreads) {
             const int tt = i / COLS, c = i % COLS;
             if (c < ncol) {
                 float o = 0.f;
 #pragma unroll
                 for (int g = 0; g < kRecThreads / 32; ++g) o += part[tt][g][c];
-                const int t = p.reverse ? len - 1 - (n0 + tt) : n0 + tt;
+                const int t = t0 + dt * (n0 + tt);
                 y[(size_t)t * p.y_tok + c] = o * p.s_out;
             }
         }
         // the staging of the next group writes sqk and sv, last read before the barrier above; `part` is written
         // again only behind the next group's first barrier
     }
-    if (tid < ncol)
-        for (int t = len; t < p.seq_len; ++t) y[(size_t)t * p.y_tok + tid] = 0.f;
-    if (p.h_last && col_ok) {
+    if (tid < ncol && sg == 0 && !quiet)
+        for (int t = all; t < p.seq_len; ++t) y[(size_t)t * p.y_tok + tid] = 0.f;
+    if (out && col_ok) {
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             const int r = rr + m * ROWS;
             if (r < p.dk) {
-                if (!p.h_t) {
-                    *reinterpret_cast<float4*>(p.h_last + sbase + (size_t)r * p.dv + c0 + cq) = s[m];
+                if (!out_t) {
+                    *reinterpret_cast<float4*>(out + (size_t)r * p.dv + c0 + cq) = s[m];
                 } else {
-                    float* a = p.h_last + sbase + (size_t)(c0 + cq) * p.dk + r;
+                    float* a = out + (size_t)(c0 + cq) * p.dk + r;
                     a[0] = s[m].x;
                     a[p.dk] = s[m].y;
                     a[2 * p.dk] = s[m].z;
@@ -267,18 +294,32 @@ __global__ void __launch_bounds__(kRecThreads, 4) linattn_step_kernel(const __gr
 
 // ------------------------------------------------------------------------------------ host
 
-// `n` passes over the same sequences and heads in one launch.  Columns per CTA: as many as the widest pass has when the
-// (sequence, head) pairs fill the GPU, fewer (down to 16) when few heads have to spread over the SMs.
-inline cudaError_t linattn_rec_launch(const LaPass* p, int n, int nsm, cudaStream_t stream) {
-    LaPasses all;
-    std::memset(&all, 0, sizeof(all));
-    int dk = 0, dv = 0;
-    for (int i = 0; i < n; ++i) {
-        all.p[i] = p[i];
-        dk = std::max(dk, p[i].dk);
-        dv = std::max(dv, p[i].dv);
-    }
-    const long long items = (long long)p[0].nseq * p[0].heads;
+// Segments of a sequence and tokens in each, for n passes of at most `width` value channels.  A token's latency (0.15 to 0.2 us)
+// bounds a run until some 2.5 CTAs of 32 columns an SM share the time; up to there sequences are divided, as finely as 14
+// CTAs an SM and 64 tokens a segment allow: the states' part of every token runs twice, but all segments at once.  Five
+// segments are the least that pay: gradients of 8 pairs, 64 x 64, 256 tokens in four 43 us, 40 undivided, 300 tokens in five
+// 45 and 48; 4000 tokens 192 and 599 (forward 76 and 599).  32 pairs, 128 x 128, 1024 tokens: 303 us and 210 in 16; their
+// gradients, which fill the SMs undivided, 564 and 548.
+inline void rec_segments(int nseq, int heads, int seq_len, int n, int width, int nsm, int& nseg, int& seg_tok) {
+    const long long ctas = (long long)nseq * heads * n * ((width + 31) / 32);
+    nseg = 1;
+    if (ctas > 0 && 2 * ctas < 5LL * nsm)
+        nseg = (int)std::min<long long>(std::min<long long>(14LL * nsm / ctas, 128), (seq_len + kLaTok - 1) / kLaTok);
+    if (nseg < 5) nseg = 1;
+    seg_tok = nseg > 1 ? (int)(((long long)seq_len + kLaTok * nseg - 1) / (kLaTok * nseg) * kLaTok) : seq_len;
+    if (nseg > 1) nseg = (int)(((long long)seq_len + seg_tok - 1) / seg_tok);
+}
+
+inline size_t rec_segment_bytes(int nseq, int heads, int seq_len, int n, int dk, int dv, int nsm) {
+    int nseg, seg_tok;
+    rec_segments(nseq, heads, seq_len, n, n > 1 ? std::max(dk, dv) : dv, nsm, nseg, seg_tok);
+    return nseg > 1 ? (size_t)n * nseq * heads * nseg * dk * dv * sizeof(float) : 0;
+}
+
+// One launch of the passes.  Columns per CTA: as many as the widest pass has when the (sequence, head, segment) triples fill
+// the GPU, fewer (down to 16) when few have to spread over the SMs.
+inline cudaError_t linattn_rec_go(const LaPasses& all, int n, int dk, int dv, int nsm, cudaStream_t stream) {
+    const long long items = (long long)all.p[0].nseq * all.p[0].heads * (all.nseg - (all.states ? 1 : 0));
     int tpr = 32;
     while (tpr > 4 && (4 * tpr >= 2 * dv || items * n * ((dv + 4 * tpr - 1) / (4 * tpr)) < 2LL * nsm)) tpr >>= 1;
     const dim3 grid((unsigned)items, (unsigned)((dv + 4 * tpr - 1) / (4 * tpr)), (unsigned)n);
@@ -297,6 +338,32 @@ inline cudaError_t linattn_rec_launch(const LaPass* p, int n, int nsm, cudaStrea
         case 8: return go(linattn_rec_kernel<8, 128>);
         default: return go(linattn_rec_kernel<4, 128>);
     }
+}
+
+// `n` passes over the same sequences and heads; seg: rec_segment_bytes bytes, or NULL when that is 0.
+inline cudaError_t linattn_rec_launch(const LaPass* p, int n, float* seg, int nsm, cudaStream_t stream) {
+    LaPasses all;
+    std::memset(&all, 0, sizeof(all));
+    int dk = 0, dv = 0;
+    for (int i = 0; i < n; ++i) {
+        all.p[i] = p[i];
+        dk = std::max(dk, p[i].dk);
+        dv = std::max(dv, p[i].dv);
+    }
+    rec_segments(p->nseq, p->heads, p->seq_len, n, dv, nsm, all.nseg, all.seg_tok);
+    if (all.nseg > 1) {
+        const size_t items = (size_t)p->nseq * p->heads, dd = (size_t)p->dk * p->dv;  // dd is the same for all passes
+        for (int i = 0; i < n; ++i) all.seg[i] = seg + i * items * all.nseg * dd;
+        all.states = 1;
+        cudaError_t e = linattn_rec_go(all, n, dk, dv, nsm, stream);
+        if (e != cudaSuccess) return e;
+        all.states = 0;
+        LaPasses scan = all;
+        for (int i = 0; i < n; ++i) scan.p[i].reverse = 0;  // segments are counted from where the scan begins
+        e = launch_pdl(linattn_segments_kernel, dim3((unsigned)((dd + 255) / 256), (unsigned)items, (unsigned)n), dim3(256), 0, stream, scan);
+        if (e != cudaSuccess) return e;
+    }
+    return linattn_rec_go(all, n, dk, dv, nsm, stream);
 }
 
 // The serving step: h0 and h_last given, one token.

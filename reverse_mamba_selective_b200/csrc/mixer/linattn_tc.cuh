@@ -46,7 +46,6 @@
 
 namespace r2l {
 
-constexpr int kLaTok = 64;        // tokens per chunk
 constexpr int kLaThreads = 512;
 constexpr int kLaBlock = 8192;    // 64 tokens x 64 channels of bf16
 
@@ -897,43 +896,6 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
     }
 }
 
-// States before the segments: seg[s] = gamma^tokens(s) seg[s - 1] + seg[s], in place (seg[0] is complete: its run
-// began with h0); and h0's copy, as it is stored, in the last place.
-__global__ void __launch_bounds__(256) linattn_segments_kernel(LaPass p, float* seg, int nseg, int seg_chunks) {
-    pdl_trigger();
-    pdl_wait();
-    const int dd = p.dk * p.dv;
-    const int e = blockIdx.x * 256 + threadIdx.x;
-    const int item = blockIdx.y;
-    if (e >= dd) return;
-    const int seq = item / p.heads, h = item - seq * p.heads;
-    const int len = la_len(p, seq), nch = (len + kLaTok - 1) / kLaTok;
-    const int missing = nch * kLaTok - len;  // tokens that the ragged chunk lacks
-    const int ragged = p.reverse ? 0 : nch - 1;
-    const float g = la_clamp_decay(p.log_decay[h]);
-    float* a = seg + (size_t)item * nseg * dd + e;
-    if (p.h0) a[(size_t)(nseg - 1) * dd] = p.h0[(size_t)item * dd + e];
-    // whole segments share a decay; eight states are on their way at once
-    const float2 whole = la_decay_pair_of(g, (float)(seg_chunks * kLaTok));
-    float s = a[0];
-    for (int i0 = 1; i0 < nseg - 1; i0 += 8) {
-        float x[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] = i0 + u < nseg - 1 ? a[(size_t)(i0 + u) * dd] : 0.f;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int i = i0 + u;
-            if (i >= nseg - 1) break;
-            const int c0 = min(i * seg_chunks, nch), c1 = min(c0 + seg_chunks, nch);
-            const int tok = (c1 - c0) * kLaTok - (ragged >= c0 && ragged < c1 ? missing : 0);
-            float2 e = whole;
-            if (tok != seg_chunks * kLaTok) la_decay_pair(g, (float)tok, e.x, e.y);
-            s = fmaf(s, e.x, fmaf(s, e.y, x[u]));
-            a[(size_t)i * dd] = s;
-        }
-    }
-}
-
 // ------------------------------------------------------------------------------------ host
 
 // [seq][token][head][channel] with the given element strides, boxes of box_rows tokens x box_cols (64 or 32) channels
@@ -1012,7 +974,13 @@ inline bool linattn_tc_launch(const LaPass& p, float* seg, int nsm, cudaStream_t
         L.nwork = p.nseq * p.heads * (L.nseg - 1);
         if (!la_tc_pick<false>(L, nsm, stream)) return false;
         const dim3 grid((unsigned)((p.dk * p.dv + 255) / 256), (unsigned)(p.nseq * p.heads));
-        if (!cuda_ok(launch_pdl(linattn_segments_kernel, grid, dim3(256), 0, stream, p, seg, L.nseg, L.seg_chunks),
+        LaPasses one;
+        std::memset(&one, 0, sizeof(one));
+        one.p[0] = p;
+        one.seg[0] = seg;
+        one.nseg = L.nseg;
+        one.seg_tok = L.seg_chunks * kLaTok;
+        if (!cuda_ok(launch_pdl(linattn_segments_kernel, grid, dim3(256), 0, stream, one),
                      "linear attention segment kernel launch"))
             return false;
     }

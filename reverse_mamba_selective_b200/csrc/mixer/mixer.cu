@@ -99,19 +99,19 @@ LaPass forward_pass(const r2l_linattn_args* a, const float* h0, float* h_last, v
     return p;
 }
 
-// Workspace of one pass (the states between a divided sequence's segments).
-size_t pass_bytes(const r2l_linattn_args* a) {
+// Workspace of n passes (the states between a divided sequence's segments): one after another in bf16, at once in fp32.
+size_t pass_bytes(const r2l_linattn_args* a, int n) {
     const int nblk = a->reverse ? a->seqlen / a->block_len : 1, len = a->seqlen / nblk;
-    if (a->dtype != R2L_BF16) return 0;
-    return align256(la_segment_bytes(a->batch * nblk, a->n_heads, len, a->d_k, a->d_v, sm_count()));
+    return align256(a->dtype == R2L_BF16 ? la_segment_bytes(a->batch * nblk, a->n_heads, len, a->d_k, a->d_v, sm_count())
+                                         : rec_segment_bytes(a->batch * nblk, a->n_heads, len, n, a->d_k, a->d_v, sm_count()));
 }
 
-// `n` passes over the same sequences and heads; seg: pass_bytes bytes, used by one after another.  fp32 runs token by
+// `n` passes over the same sequences and heads; seg: pass_bytes bytes.  fp32 runs token by
 // token; bf16 in chunks, short blocks by the kernels for them (the gradients of a block with a state transpose it,
 // which the resuming kernel does not).
 bool run_passes(const LaPass* p, int n, r2l_dtype dtype, void* seg, cudaStream_t stream) {
     const int nsm = sm_count();
-    if (dtype == R2L_F32) return cuda_ok(linattn_rec_launch(p, n, nsm, stream), "linear attention kernel launch");
+    if (dtype == R2L_F32) return cuda_ok(linattn_rec_launch(p, n, static_cast<float*>(seg), nsm, stream), "linear attention kernel launch");
     bool state = false;
     for (int i = 0; i < n; ++i) state = state || p[i].h0 || p[i].h_last;
     if (!state && p->seq_len <= kBlkMaxTok)
@@ -159,7 +159,7 @@ extern "C" {
 
 size_t r2l_linattn_workspace_size(const r2l_linattn_args* a) {
     if (check_linattn(a) != R2L_OK || la_empty(a) || a->seqlen == 0) return 0;
-    return pass_bytes(a);
+    return pass_bytes(a, 1);
 }
 
 r2l_status r2l_linattn(const r2l_linattn_args* a, const float* h0, float* h_last, void* y, void* workspace,
@@ -190,7 +190,7 @@ r2l_status r2l_linattn_step(const r2l_linattn_args* a, const float* h, float* h_
 
 size_t r2l_linattn_bwd_workspace_size(const r2l_linattn_args* a) {
     if (check_linattn(a) != R2L_OK || la_empty(a) || a->seqlen == 0) return 0;
-    return bwd_parts(a).total + pass_bytes(a);
+    return bwd_parts(a).total + pass_bytes(a, 3);
 }
 
 r2l_status r2l_linattn_bwd(const r2l_linattn_args* a, const void* dy, const float* h0, const float* dh_last, void* dq,

@@ -201,3 +201,11 @@ def test_binding_refusals(r2l):
         with pytest.raises(err):
             bad()
     ok()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("L,H,kh,dk,dv", [(1300, 2, 1, 64, 48), (2111, 1, 1, 128, 32)])
+def test_divided_sequences_of_a_padded_batch(r2l, L, H, kh, dk, dv, dtype, reverse):
+    # divided over the SMs; rows that end before, at and inside a segment's first token
+    check(r2l, dict(b=4, L=L, H=H, qh=kh, kh=kh, dk=dk, dv=dv, dtype=dtype, reverse=reverse, lens=[0, 193, L // 2, L], h0=True), seed=L)
