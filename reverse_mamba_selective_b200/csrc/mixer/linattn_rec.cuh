@@ -7,10 +7,11 @@
 // joined by a reduce-scatter of shuffles, those of the 8 warps in shared memory, kRecTok tokens at a time (two
 // barriers), while the next tokens are on their way into registers.
 //
-// Runs in fp32 are bound by the FMA pipe where (sequence, head) pairs fill the GPU (4 operations an element and token),
-// else by the latency of a token; then the columns are spread over more CTAs, the instructions of four tokens run
-// into each other, and long sequences are divided.  Gradients of 2 x 8 sequences and heads of 200 tokens, 64 x 48: 44 us, 0.2 us a token of one pass (61 us
-// a token at a time).  The step is bound by memory: 2048 states of 128 x 128, 44 us in and out, 6.1 TB/s.
+// Where (sequence, head) pairs fill the GPU, a run in fp32 takes a third of the FMA rate (4 operations an element and
+// token, paired): 64 pairs of 1000 tokens, 128 x 128, 371 us (418 unpaired), two CTAs an SM by their registers.  Else it is
+// bound by the latency of a token; then the columns are spread over more CTAs, the instructions of four tokens run into
+// each other, and long sequences are divided.  Gradients of 2 x 8 sequences and heads of 200 tokens, 64 x 48: 44 us,
+// 0.2 us a token of one pass (61 us a token at a time).  The step is bound by memory: 2048 states of 128 x 128, 44 us in and out, 6.1 TB/s.
 #pragma once
 
 #include <algorithm>
@@ -18,12 +19,23 @@
 #include <type_traits>
 
 #include "linattn_common.cuh"
+#include "pairs.cuh"
 
 namespace r2l {
 
 constexpr int kRecThreads = 256;
 constexpr int kRecTok = 8;       // tokens staged at once: one a warp
 constexpr int kRecMaxD = 128;
+
+__device__ __forceinline__ float4 rec_fma(float4 a, float b, float4 c) {
+    const float2 x = fma2(make_float2(a.x, a.y), make_float2(b, b), make_float2(c.x, c.y));
+    const float2 y = fma2(make_float2(a.z, a.w), make_float2(b, b), make_float2(c.z, c.w));
+    return make_float4(x.x, x.y, y.x, y.y);
+}
+__device__ __forceinline__ float4 rec_mul(float4 a, float b) {
+    const float2 x = mul2(make_float2(a.x, a.y), make_float2(b, b)), y = mul2(make_float2(a.z, a.w), make_float2(b, b));
+    return make_float4(x.x, x.y, y.x, y.y);
+}
 
 // DK: 64 or 128, the passes' key channels at most.
 template <int TPR, int DK>
@@ -130,26 +142,12 @@ __global__ void __launch_bounds__(kRecThreads) linattn_rec_kernel(const __grid_c
                 for (int m = 0; m < M; ++m) {
                     const float2 qk = sqk[tt][rr + m * ROWS];
                     float4 a = s[m];
-                    if constexpr (SHIFT) {
-                        a = make_float4(fmaf(qk.y, vv.x, a.x), fmaf(qk.y, vv.y, a.y), fmaf(qk.y, vv.z, a.z), fmaf(qk.y, vv.w, a.w));
-                    } else {
-                        a.x = fmaf(a.x, ghi, fmaf(a.x, glo, qk.y * vv.x));
-                        a.y = fmaf(a.y, ghi, fmaf(a.y, glo, qk.y * vv.y));
-                        a.z = fmaf(a.z, ghi, fmaf(a.z, glo, qk.y * vv.z));
-                        a.w = fmaf(a.w, ghi, fmaf(a.w, glo, qk.y * vv.w));
-                    }
-                    if constexpr (!QUIET) {
-                        o.x = fmaf(qk.x, a.x, o.x);
-                        o.y = fmaf(qk.x, a.y, o.y);
-                        o.z = fmaf(qk.x, a.z, o.z);
-                        o.w = fmaf(qk.x, a.w, o.w);
-                    }
-                    if constexpr (SHIFT) {
-                        a.x = fmaf(a.x, ghi, a.x * glo);
-                        a.y = fmaf(a.y, ghi, a.y * glo);
-                        a.z = fmaf(a.z, ghi, a.z * glo);
-                        a.w = fmaf(a.w, ghi, a.w * glo);
-                    }
+                    if constexpr (SHIFT)
+                        a = rec_fma(vv, qk.y, a);
+                    else
+                        a = rec_fma(a, ghi, rec_fma(a, glo, rec_mul(vv, qk.y)));
+                    if constexpr (!QUIET) o = rec_fma(a, qk.x, o);
+                    if constexpr (SHIFT) a = rec_fma(a, ghi, rec_mul(a, glo));
                     s[m] = a;
                 }
                 // the warp's W rows: each step halves what a lane sums, down to one column a lane
@@ -298,7 +296,7 @@ __global__ void __launch_bounds__(kRecThreads, 4) linattn_step_kernel(const __gr
 // bounds a run until some 2.5 CTAs of 32 columns an SM share the time; up to there sequences are divided, as finely as 14
 // CTAs an SM and 64 tokens a segment allow: the states' part of every token runs twice, but all segments at once.  Five
 // segments are the least that pay: gradients of 8 pairs, 64 x 64, 256 tokens in four 43 us, 40 undivided, 300 tokens in five
-// 45 and 48; 4000 tokens 192 and 599 (forward 76 and 599).  32 pairs, 128 x 128, 1024 tokens: 303 us and 210 in 16; their
+// 45 and 48; 4000 tokens 183 and 599 (forward 75 and 599).  32 pairs, 128 x 128, 1024 tokens: 303 us and 210 in 16; their
 // gradients, which fill the SMs undivided, 564 and 548.
 inline void rec_segments(int nseq, int heads, int seq_len, int n, int width, int nsm, int& nseg, int& seg_tok) {
     const long long ctas = (long long)nseq * heads * n * ((width + 31) / 32);
