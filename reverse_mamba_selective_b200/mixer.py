@@ -182,19 +182,20 @@ def _heads(name: str, t: torch.Tensor, dtype, lead: Tuple[int, ...], index: int)
     heads, d = shape[-2], shape[-1]
     if (d > 1 and strides[-1] != 1) or (heads > 1 and strides[-2] != d):
         raise ValueError(f"{name} must have dense heads and channels")
-    # the innermost dimension of lead that has more than one entry gives the tokens' distance, the others follow from it
-    tok, want = 0, 0
+    # the innermost dimension of lead that has more than one entry gives the tokens' distance (none has: dense), the others
+    # follow from it; a distance of 0 is a broadcast, whose tokens the library would read as dense
+    tok = want = None
     for n, st in zip(reversed(lead), reversed(strides[:-2])):
-        if want == 0:
-            if n > 1:
-                tok, want = st, st * n
+        if n == 1:
             continue
-        if n > 1 and st != want:
+        if tok is None:
+            if st < heads * d:
+                raise ValueError(f"{name} must not have overlapping tokens")
+            tok = want = st
+        elif st != want:
             raise ValueError(f"{name} must have its tokens evenly spaced")
         want *= n
-    if tok and tok < heads * d:
-        raise ValueError(f"{name} must not have overlapping tokens")
-    return tok
+    return tok or 0
 
 
 def _linattn_args(q, k, v, log_decay, scale, block_len, reverse, seq_lens, lead, index) -> LinattnArgs:
@@ -372,20 +373,17 @@ def r2l_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.
     lib = load_mixer()
     index = _first("q", q, 3)
     a = _rope_args(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, index)
-    qs = ks = 0
+    qs = 0 if q_out is None else _heads("q_out", q_out, q.dtype, (a.tokens,), index)
+    ks = 0 if k_out is None else _heads("k_out", k_out, q.dtype, (a.tokens,), index)
+    for name, o, t in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if o is not None and o.shape != t.shape:
+            raise ValueError(f"{name} must have shape {tuple(t.shape)}, got {tuple(o.shape)}")
     made_q = made_k = None
     with _on_device(index):
         if q_out is None:
             q_out = made_q = _dense(q, q.shape)
-        else:
-            qs = _heads("q_out", q_out, q.dtype, (a.tokens,), index)
         if k_out is None:
             k_out = made_k = _dense(k, k.shape)
-        else:
-            ks = _heads("k_out", k_out, q.dtype, (a.tokens,), index)
-        for name, o, t in (("q_out", q_out, q), ("k_out", k_out, k)):
-            if o.shape != t.shape:
-                raise ValueError(f"{name} must have shape {tuple(t.shape)}, got {tuple(o.shape)}")
         st = lib.r2l_qk_norm_rope(ctypes.byref(a), q_out.data_ptr(), qs, k_out.data_ptr(), ks,
                                   _stream_of(stream, index, made_q, made_k))
     if st != R2L_OK:

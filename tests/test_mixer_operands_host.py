@@ -1,0 +1,103 @@
+"""What the mixer binding makes of its operands' strides, without a GPU: tensors of the CPU that say they are on cuda:0, and
+calls that are refused before anything is launched."""
+
+import pytest
+import torch
+
+
+class OnCuda(torch.Tensor):
+    """A CPU tensor that the binding takes for one on cuda:0."""
+
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def cuda(t):
+    return t.as_subclass(OnCuda)
+
+
+@pytest.fixture(scope="module")
+def r2l():
+    from reverse_mamba_selective_b200 import _build
+
+    _build.build()
+    import reverse_mamba_selective_b200 as pkg
+
+    pkg.load_mixer()
+    return pkg
+
+
+def tokens(*lead, heads=4, d=64):
+    return torch.zeros(*lead, heads, d, dtype=torch.bfloat16)
+
+
+# what lies in memory, and the tokens it is broadcast to
+BROADCAST = [((1, 1), (1, 50)), ((3, 1), (3, 50)), ((1, 1), (3, 50)), ((1, 50), (3, 50)), ((1, 1), (8, 1)), ((1,), (128,))]
+
+
+@pytest.mark.parametrize("held,lead", BROADCAST)
+def test_tokens_that_share_their_memory_are_refused(held, lead):
+    from reverse_mamba_selective_b200 import mixer
+
+    t = cuda(tokens(*held)).expand(*lead, 4, 64)
+    with pytest.raises(ValueError):
+        mixer._heads("x", t, torch.bfloat16, lead, 0)
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("held,lead", BROADCAST)
+def test_no_entry_point_takes_a_broadcast_operand(r2l, held, lead, which):
+    x = [cuda(tokens(*lead)) for _ in range(3)]
+    x[which] = cuda(tokens(*held)).expand(*lead, 4, 64)
+    g = cuda(torch.zeros(4))
+    with pytest.raises(ValueError):
+        if len(lead) == 2:
+            r2l.r2l_linattn(*x, g)
+        else:
+            r2l.r2l_linattn_step(*x, g, cuda(torch.zeros(lead[0], 4, 64, 64)))
+    if len(lead) == 2:
+        with pytest.raises(ValueError):
+            r2l.r2l_linattn_bwd(*x, g, cuda(tokens(*lead)))
+
+
+@pytest.mark.parametrize("which", ["q", "k", "q_out", "k_out"])
+def test_norm_and_rotation_take_no_broadcast_operand_or_output(r2l, which):
+    x = {n: cuda(tokens(20)) for n in ("q", "k", "q_out", "k_out")}
+    x[which] = cuda(tokens(1)).expand(20, 4, 64)
+    with pytest.raises(ValueError):
+        r2l.r2l_qk_norm_rope(x["q"], x["k"], None, None, None, None, q_out=x["q_out"], k_out=x["k_out"])
+    if which in ("q", "k"):
+        with pytest.raises(ValueError):
+            r2l.r2l_qk_norm_rope_bwd(x["q"], x["k"], None, None, None, None, cuda(tokens(20)), cuda(tokens(20)))
+
+
+@pytest.mark.parametrize("make,lead,stride", [
+    (lambda: tokens(3, 50), (3, 50), 0),
+    (lambda: tokens(3, 50, heads=9)[:, :, 2:6], (3, 50), 9 * 64),
+    (lambda: tokens(3, 50, heads=9)[:1, :, 2:6], (1, 50), 9 * 64),
+    (lambda: tokens(3, 50, heads=9)[:, :1, 2:6], (3, 1), 50 * 9 * 64),
+    (lambda: tokens(3, 50, heads=9)[:, 7, 2:6], (3,), 50 * 9 * 64),
+    (lambda: tokens(3, 50, heads=9)[1:2, 7, 2:6], (1,), 0),
+    (lambda: tokens(1, 1).expand(1, 1, 4, 64), (1, 1), 0),
+    (lambda: tokens(3, 50)[:, ::2], (3, 25), 2 * 4 * 64),
+    (lambda: tokens(0, 50), (0, 50), 0),
+])
+def test_tokens_with_memory_of_their_own_are_taken(make, lead, stride):
+    from reverse_mamba_selective_b200 import mixer
+
+    assert mixer._heads("x", cuda(make()), torch.bfloat16, lead, 0) == stride
+
+
+@pytest.mark.parametrize("make,lead", [
+    (lambda: tokens(3, 50)[:, :49], (3, 49)),                         # rows further apart than their tokens say
+    (lambda: tokens(50, 3).transpose(0, 1), (3, 50)),                 # tokens of a row further apart than the rows
+    (lambda: tokens(3, 50).transpose(2, 3), (3, 50)),                 # channels not dense
+    (lambda: torch.zeros(4000, dtype=torch.bfloat16).as_strided((5, 4, 64), (128, 64, 1)), (5,)),  # tokens that overlap in part
+])
+def test_tokens_not_evenly_spaced_are_refused(make, lead):
+    from reverse_mamba_selective_b200 import mixer
+
+    with pytest.raises(ValueError):
+        mixer._heads("x", cuda(make()), torch.bfloat16, lead, 0)
