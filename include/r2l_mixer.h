@@ -50,6 +50,9 @@ extern "C" {
  *   row's own tokens.  Reverse runs start at token seq_lens[b] - 1.  Not with blocks (block_len must be
  *   seqlen in reverse runs).
  *
+ * Sums over nothing are zero: with n_heads, d_k or d_v 0, those outputs that are not empty all the same (y and dv
+ * without key channels, dq and dk without value channels) are set to zero, or may be NULL.
+ *
  * Requirements: dtype R2L_F32 or R2L_BF16; d_k and d_v at most 128 and multiples of 8 (bf16) or 4 (fp32);
  * strides multiples of 8 (bf16) or 4 (fp32) and no smaller than the token's heads; q, k, v, y and the states
  * 16-byte aligned.

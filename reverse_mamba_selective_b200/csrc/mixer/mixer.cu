@@ -132,6 +132,13 @@ r2l_status copy_state(const float* h0, float* h_last, size_t n, cudaStream_t str
                : R2L_ERR_CUDA;
 }
 
+// An output [batch][seqlen][heads][d] whose sums have no terms (no heads, or no channels to sum over): zeros.
+r2l_status zero_output(const r2l_linattn_args* a, void* out, int heads, int d, cudaStream_t stream) {
+    if (!out || heads <= 0 || d == 0) return R2L_OK;
+    // d is a multiple of 16 bytes
+    return copy_state(nullptr, static_cast<float*>(out), (size_t)a->batch * a->seqlen * heads * (d * esize(a->dtype) / 4), stream);
+}
+
 // Workspace of the backward call: per-head fp32 gradients of those of q, k, v whose heads are shared.
 struct BwdParts {
     size_t off[3], total;
@@ -168,7 +175,7 @@ r2l_status r2l_linattn(const r2l_linattn_args* a, const float* h0, float* h_last
     if (st != R2L_OK) return st;
     if ((h0 || h_last) && !carries_state(a)) return R2L_ERR_INVALID_ARG;
     if (!aligned16(h0) || !aligned16(h_last)) return R2L_ERR_INVALID_ARG;
-    if (la_empty(a)) return R2L_OK;
+    if (la_empty(a)) return aligned16(y) ? zero_output(a, y, a->n_heads, a->d_v, stream) : R2L_ERR_INVALID_ARG;
     if (a->seqlen == 0) return copy_state(h0, h_last, (size_t)a->batch * a->n_heads * a->d_k * a->d_v, stream);
     if (!y || !aligned16(y)) return R2L_ERR_INVALID_ARG;
     if (bad_workspace(workspace, workspace_bytes, r2l_linattn_workspace_size(a))) return R2L_ERR_INVALID_ARG;
@@ -180,7 +187,7 @@ r2l_status r2l_linattn_step(const r2l_linattn_args* a, const float* h, float* h_
     r2l_status st = check_linattn(a);
     if (st != R2L_OK) return st;
     if (a->seqlen != 1 || a->reverse || a->seq_lens) return R2L_ERR_INVALID_ARG;
-    if (la_empty(a)) return R2L_OK;
+    if (la_empty(a)) return aligned16(y) ? zero_output(a, y, a->n_heads, a->d_v, stream) : R2L_ERR_INVALID_ARG;
     if (!h || !h_out || !y || !aligned16(h) || !aligned16(h_out) || !aligned16(y)) return R2L_ERR_INVALID_ARG;
     const LaPass p = forward_pass(a, h, h_out, y);
     const cudaError_t e = a->dtype == R2L_F32 ? linattn_step_launch<float>(p, sm_count(), stream)
@@ -200,7 +207,12 @@ r2l_status r2l_linattn_bwd(const r2l_linattn_args* a, const void* dy, const floa
     if ((h0 || dh_last || dh0) && !carries_state(a)) return R2L_ERR_INVALID_ARG;
     if (!aligned16(h0) || !aligned16(dh_last) || !aligned16(dh0)) return R2L_ERR_INVALID_ARG;
     if (dh0 && (dh0 == dh_last || dh0 == h0)) return R2L_ERR_INVALID_ARG;
-    if (la_empty(a)) return R2L_OK;
+    if (la_empty(a)) {
+        if (!aligned16(dq) || !aligned16(dk) || !aligned16(dv)) return R2L_ERR_INVALID_ARG;
+        if ((st = zero_output(a, dq, a->q_heads, a->d_k, stream)) != R2L_OK) return st;
+        if ((st = zero_output(a, dk, a->k_heads, a->d_k, stream)) != R2L_OK) return st;
+        return zero_output(a, dv, a->v_heads, a->d_v, stream);
+    }
     if (a->seqlen == 0) return copy_state(dh_last, dh0, (size_t)a->batch * a->n_heads * a->d_k * a->d_v, stream);
     for (const void* q : {dy, (const void*)dq, (const void*)dk, (const void*)dv})
         if (!q || !aligned16(q)) return R2L_ERR_INVALID_ARG;

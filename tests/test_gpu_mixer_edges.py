@@ -1,0 +1,38 @@
+"""The mixer's operators at the edges of what their documentation allows: sums over nothing, infinite states, streams that
+the outputs are made for, the longest rows.  Reference and tolerances are those of test_gpu_linattn.py."""
+
+import pytest
+import torch
+
+import mixer_ref as R
+from test_gpu_linattn import DEV, TYPES, r2l  # noqa: F401  (r2l is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def dirty(*sizes):
+    """Leaves blocks full of ones with the allocator, so that memory that is not written shows."""
+    blocks = [torch.ones(max(n, 1), device=DEV) for n in sizes for _ in range(4)]
+    torch.cuda.synchronize()
+    del blocks
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv,H", [(0, 64, 2), (64, 0, 2), (0, 0, 2), (64, 64, 0)])
+def test_sums_over_nothing_are_zero(r2l, dtype, dk, dv, H):
+    b, L, t = 2, 70, TYPES[dtype]
+    q, k = (torch.ones(b, L, 2, dk, dtype=t, device=DEV) for _ in range(2))
+    v = torch.ones(b, L, 2, dv, dtype=t, device=DEV)
+    g = R.log_decays(H).to(DEV)
+    h0 = torch.ones(b, H, dk, dv, device=DEV)
+    zeros = lambda x: x is not None and torch.equal(x, torch.zeros_like(x))
+    dirty(b * L * 64, b * L * 128)
+    y, h = r2l.r2l_linattn(q, k, v, g, h0=h0, want_h_last=True)
+    assert y.shape == (b, L, H, dv) and zeros(y) and h.shape == (b, H, dk, dv)
+    y = torch.ones(b, L, H, dv, dtype=t, device=DEV)
+    assert zeros(r2l.r2l_linattn(q, k, v, g, reverse=True, block_len=10, y=y)[0])
+    y = torch.ones(b, H, dv, dtype=t, device=DEV)
+    assert zeros(r2l.r2l_linattn_step(q[:, 0], k[:, 0], v[:, 0], g, h0, y=y))
+    dirty(b * L * 64, b * L * 128)
+    got = r2l.r2l_linattn_bwd(q, k, v, g, torch.ones(b, L, H, dv, dtype=t, device=DEV), h0=h0)
+    assert zeros(got["dq"]) and zeros(got["dk"]) and zeros(got["dv"]) and got["dh0"].shape == h0.shape

@@ -1,6 +1,8 @@
 """What the mixer binding makes of its operands' strides, without a GPU: tensors of the CPU that say they are on cuda:0, and
 calls that are refused before anything is launched."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -101,3 +103,37 @@ def test_tokens_not_evenly_spaced_are_refused(make, lead):
 
     with pytest.raises(ValueError):
         mixer._heads("x", cuda(make()), torch.bfloat16, lead, 0)
+
+
+def args(r2l, **over):
+    a = dict(batch=2, seqlen=6, block_len=6, n_heads=4, q_heads=4, k_heads=2, v_heads=4, d_k=64, d_v=32, reverse=0,
+             dtype=r2l.R2L_BF16, scale=0.125, q=4096, k=8192, v=12288, q_stride=0, k_stride=0, v_stride=0, log_decay=256,
+             seq_lens=None)
+    a.update(over)
+    return r2l.LinattnArgs(**a)
+
+
+@pytest.mark.parametrize("over", [dict(d_k=0), dict(d_v=0), dict(n_heads=0)])
+def test_outputs_of_empty_sums_are_checked(r2l, over):
+    lib = r2l.load_mixer()
+    a = args(r2l, **over)
+    one = args(r2l, **over, seqlen=1, block_len=1)
+    assert lib.r2l_linattn(ctypes.byref(a), None, None, 16392, None, 0, None) == r2l.R2L_ERR_INVALID_ARG
+    assert lib.r2l_linattn_step(ctypes.byref(one), 4096, 4096, 16392, None) == r2l.R2L_ERR_INVALID_ARG
+    for o in ((8, None, None), (None, 8, None), (None, None, 8)):
+        assert lib.r2l_linattn_bwd(ctypes.byref(a), 16384, None, None, *o, None, None, 0, None) == r2l.R2L_ERR_INVALID_ARG
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the behaviour on a machine without a GPU")
+def test_outputs_of_empty_sums_are_written(r2l):
+    """Zeros have to be written where an output is not empty: without a GPU that fails, and does not pass in silence."""
+    lib = r2l.load_mixer()
+    run = lambda y, **over: lib.r2l_linattn(ctypes.byref(args(r2l, **over)), None, None, y, None, 0, None)
+    assert run(16384, d_k=0) == r2l.R2L_ERR_CUDA
+    assert run(16384, d_v=0) == run(16384, n_heads=0) == run(16384, d_k=0, seqlen=0) == run(None, d_k=0) == r2l.R2L_OK
+    one = dict(seqlen=1, block_len=1)
+    step = lambda **over: lib.r2l_linattn_step(ctypes.byref(args(r2l, **one, **over)), 4096, 4096, 16384, None)
+    assert step(d_k=0) == r2l.R2L_ERR_CUDA and step(d_v=0) == r2l.R2L_OK
+    grad = lambda dq, dk, dv, **over: lib.r2l_linattn_bwd(ctypes.byref(args(r2l, **over)), 16384, None, None, dq, dk, dv, None, None, 0, None)
+    assert grad(None, None, 16384, d_k=0) == grad(16384, None, None, d_v=0) == grad(None, 16384, None, d_v=0) == r2l.R2L_ERR_CUDA
+    assert grad(16384, 32768, None, d_k=0) == grad(None, None, 16384, d_v=0) == r2l.R2L_OK
