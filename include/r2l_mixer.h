@@ -54,8 +54,8 @@ extern "C" {
  * without key channels, dq and dk without value channels) are set to zero, or may be NULL.
  *
  * Requirements: dtype R2L_F32 or R2L_BF16; d_k and d_v at most 128 and multiples of 8 (bf16) or 4 (fp32);
- * strides multiples of 8 (bf16) or 4 (fp32) and no smaller than the token's heads; q, k, v, y and the states
- * 16-byte aligned.
+ * strides multiples of 8 (bf16) or 4 (fp32) and no smaller than the token's heads; batch * seqlen less than
+ * 2^31 - 256 tokens; q, k, v, y and the states 16-byte aligned.
  */
 typedef struct {
     int batch, seqlen, block_len;

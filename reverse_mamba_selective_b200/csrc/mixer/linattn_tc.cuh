@@ -265,6 +265,17 @@ __device__ __noinline__ void la_zero_rows(unsigned char* v, int vb, int n, int t
     }
 }
 
+// Rows t0 .. of a sequence's outputs become zeros, by 128 threads: 16-byte pieces (dv is a multiple of 8, 32 pieces a row at
+// most).  Rows and pieces are counted apart: their product may pass 2^31.
+__device__ __noinline__ void la_zero_tail(const LaPass& p, int seq, int h, int t0, int tid) {
+    const int es = p.y_f32 ? 4 : 2, per_row = p.dv * es / 16, rows = p.seq_len - t0, rows_par = 128 / per_row;
+    const int first = tid / per_row, piece = tid - first * per_row;
+    if (first >= rows_par) return;
+    unsigned char* y = static_cast<unsigned char*>(p.y) +
+                       (((size_t)seq * p.seq_len + t0) * p.y_tok + (size_t)h * p.dv) * es + piece * 16;
+    for (int t = first; t < rows; t += rows_par) *reinterpret_cast<uint4*>(y + (size_t)t * p.y_tok * es) = make_uint4(0, 0, 0, 0);
+}
+
 // r += fac * s2 on fragments: a column pair's factors are those of its tokens.
 __device__ __forceinline__ void la_add_inter(uint32_t (&r)[32], const uint32_t (&s2)[32], const float2 (&fac)[8]) {
 #pragma unroll
@@ -775,16 +786,8 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[st]);
             }
-            if (it.a == 0 && ok) {  // chunks that lie wholly behind the row's tokens: zeros
-                // 16-byte pieces, the four warps' threads over rows and pieces (dv is a multiple of 8)
-                const int es = p.y_f32 ? 4 : 2, per_row = p.dv * es / 16, t0 = it.nch * kLaTok;
-                unsigned char* y = static_cast<unsigned char*>(p.y) +
-                                   (((size_t)it.seq * p.seq_len + t0) * p.y_tok + (size_t)it.h * p.dv) * es;
-                for (int i = tid - 256; i < (p.seq_len - t0) * per_row; i += 128) {
-                    const int t = i / per_row;
-                    *reinterpret_cast<uint4*>(y + (size_t)t * p.y_tok * es + (i - t * per_row) * 16) = make_uint4(0, 0, 0, 0);
-                }
-            }
+            // chunks that lie wholly behind the row's tokens: zeros
+            if (it.a == 0 && ok && it.nch * kLaTok < p.seq_len) la_zero_tail(p, it.seq, it.h, it.nch * kLaTok, tid - 256);
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     } else if (Y && warp < 14) {

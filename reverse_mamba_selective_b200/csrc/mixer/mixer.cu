@@ -60,7 +60,8 @@ r2l_status check_linattn(const r2l_linattn_args* a) {
         if (strides[i] != 0 && (strides[i] < dense[i] || strides[i] % vec != 0 || strides[i] > (1LL << 38)))
             return R2L_ERR_INVALID_ARG;
     if (la_empty(a)) return R2L_OK;
-    if ((long long)a->batch * a->seqlen > INT_MAX || (long long)a->batch * a->n_heads > INT_MAX) return R2L_ERR_UNSUPPORTED;
+    // the kernels' token counters run a few chunks past the last token
+    if ((long long)a->batch * a->seqlen > INT_MAX - 256 || (long long)a->batch * a->n_heads > INT_MAX) return R2L_ERR_UNSUPPORTED;
     const long long nblk = a->reverse && a->seqlen > 0 ? a->seqlen / a->block_len : 1;
     if (a->batch * nblk * a->n_heads > INT_MAX) return R2L_ERR_UNSUPPORTED;
     if (!a->log_decay || (reinterpret_cast<uintptr_t>(a->log_decay) & 3u)) return R2L_ERR_INVALID_ARG;

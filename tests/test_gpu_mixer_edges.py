@@ -36,3 +36,25 @@ def test_sums_over_nothing_are_zero(r2l, dtype, dk, dv, H):
     dirty(b * L * 64, b * L * 128)
     got = r2l.r2l_linattn_bwd(q, k, v, g, torch.ones(b, L, H, dv, dtype=t, device=DEV), h0=h0)
     assert zeros(got["dq"]) and zeros(got["dk"]) and zeros(got["dv"]) and got["dh0"].shape == h0.shape
+
+
+def test_rows_of_more_pieces_than_32_bits_count(r2l):
+    """A short sequence in a row of 2^27 tokens and more: 2^31 16-byte pieces of zeros stand behind it."""
+    L, n, d = 2 ** 27 + 2 ** 20, 100, 128
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB of device memory")
+    gen = torch.Generator().manual_seed(1)
+    first = [torch.randn(1, n, 1, w, generator=gen).to(torch.bfloat16).to(DEV) for w in (8, 8, d)]
+    g = torch.tensor([-0.1], device=DEV)
+    want = r2l.r2l_linattn(*first, g)[0]
+    q, k, v = (torch.empty(1, L, 1, w, dtype=torch.bfloat16, device=DEV) for w in (8, 8, d))  # what padding holds does not count
+    for x, f in zip((q, k, v), first):
+        x[:, :n] = f
+    y = torch.ones(1, L, 1, d, dtype=torch.bfloat16, device=DEV)
+    r2l.r2l_linattn(q, k, v, g, seq_lens=torch.tensor([n], dtype=torch.int32, device=DEV), y=y)
+    # two results, each rounded by half a step at most
+    assert R.rel_err_per_head(y[:, :n], want) <= 2 * 2.0 ** -8
+    bits = y[:, n:].view(torch.int32)
+    assert int(bits.amax()) == int(bits.amin()) == 0
+    del q, k, v, y, bits
+    torch.cuda.empty_cache()

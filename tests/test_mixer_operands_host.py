@@ -137,3 +137,15 @@ def test_outputs_of_empty_sums_are_written(r2l):
     grad = lambda dq, dk, dv, **over: lib.r2l_linattn_bwd(ctypes.byref(args(r2l, **over)), 16384, None, None, dq, dk, dv, None, None, 0, None)
     assert grad(None, None, 16384, d_k=0) == grad(16384, None, None, d_v=0) == grad(None, 16384, None, d_v=0) == r2l.R2L_ERR_CUDA
     assert grad(16384, 32768, None, d_k=0) == grad(None, None, 16384, d_v=0) == r2l.R2L_OK
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_rows_at_the_end_of_the_token_counters(r2l, dtype):
+    """The kernels count tokens in 32 bits, some chunks ahead: runs that would pass the end are refused."""
+    lib = r2l.load_mixer()
+    size = lambda n, b=1: lib.r2l_linattn_workspace_size(ctypes.byref(args(r2l, batch=b, seqlen=n, block_len=n, dtype=dtype)))
+    run = lambda n, b=1: lib.r2l_linattn(ctypes.byref(args(r2l, batch=b, seqlen=n, block_len=n, dtype=dtype)), None, None, 16384,
+                                         1 << 20, 1 << 40, None)
+    for n, b in ((2 ** 31 - 1, 1), (2 ** 31 - 8, 1), (2 ** 31 - 256, 1), (2 ** 30, 2)):
+        assert run(n, b) == r2l.R2L_ERR_UNSUPPORTED and size(n, b) == 0
+    assert size(2 ** 31 - 257) > 0
