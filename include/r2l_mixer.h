@@ -50,6 +50,9 @@ extern "C" {
  *   row's own tokens.  Reverse runs start at token seq_lens[b] - 1.  Not with blocks (block_len must be
  *   seqlen in reverse runs).
  *
+ * Infinities: one in a state stays there under any decay but 0, and reaches the outputs as the formulas say.  What an
+ * infinite k or v token leaves in a state is not finite, but bf16 runs may leave NaN where the formulas give an infinity.
+ *
  * Sums over nothing are zero: with n_heads, d_k or d_v 0, those outputs that are not empty all the same (y and dv
  * without key channels, dq and dk without value channels) are set to zero, or may be NULL.
  *

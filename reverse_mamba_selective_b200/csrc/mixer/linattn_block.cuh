@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(2 * DV, ResumeCfg<DK, DV>::Ctas) linattn_resum
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     const float *x = &S[2 * k][n * 2], *y = &S[2 * k + 1][n * 2];
-                    const uint32_t b0 = blk_pack(x[0], x[1]), b1 = blk_pack(y[0], y[1]);
+                    const uint32_t b0 = la_pack_sat(x[0], x[1]), b1 = la_pack_sat(y[0], y[1]);
                     blk_mma(o[n], a, b0, b1);
                     blk_mma(a2[n], a, blk_pack(x[0] - blk_lo(b0), x[1] - blk_hi(b0)), blk_pack(y[0] - blk_lo(b1), y[1] - blk_hi(b1)));
                 }

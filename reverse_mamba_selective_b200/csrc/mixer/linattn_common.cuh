@@ -45,18 +45,28 @@ __device__ __forceinline__ float la_decay_pow_of(float g, float n) {
 // Not inlined: for tables that are built once a head.
 __device__ __noinline__ float la_decay_pow(float g, float n) { return la_decay_pow_of(g, n); }
 
-// e^(g n) as the sum of two fp32 numbers: a state that is multiplied by it thousands of times keeps fp32
-// precision (one fp32 factor is 2^-25 off, the same way each time: 2.4e-4 after 8192 tokens).
-__device__ __forceinline__ float2 la_decay_pair_of(float g, float n) {
-    const double e = exp((double)g * (double)n);
-    const float hi = (float)e;
-    return make_float2(hi, (float)(e - (double)hi));
+// e as the sum of two fp32 numbers, neither negative, the second not zero: an infinite state times both stays what it is
+// (times zero, or with the signs apart, it would become NaN).
+__device__ __forceinline__ float2 la_two_parts(double e) {
+    const float hi = __double2float_rz(e), lo = (float)(e - (double)hi);
+    return make_float2(hi, hi > 0.f ? fmaxf(lo, __uint_as_float(1u)) : lo);
 }
+// e^(g n) in two parts: a state that is multiplied by it thousands of times keeps fp32 precision (one fp32 factor is
+// 2^-25 off, the same way each time: 2.4e-4 after 8192 tokens).
+__device__ __forceinline__ float2 la_decay_pair_of(float g, float n) { return la_two_parts(exp((double)g * (double)n)); }
 __device__ __noinline__ float2 la_decay_pair_call(float g, float n) { return la_decay_pair_of(g, n); }
 __device__ __forceinline__ void la_decay_pair(float g, float n, float& hi, float& lo) {
     const float2 e = la_decay_pair_call(g, n);
     hi = e.x;
     lo = e.y;
+}
+
+// Two fp32 values rounded to bf16, infinities to the largest number: the first part of a split leaves an infinity to the
+// second, where plain rounding would leave it inf - inf.
+__device__ __forceinline__ uint32_t la_pack_sat(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
 }
 
 __device__ __forceinline__ int la_len(const LaPass& p, int seq) {

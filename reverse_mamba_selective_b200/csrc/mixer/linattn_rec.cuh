@@ -256,9 +256,9 @@ __global__ void __launch_bounds__(kRecThreads, 4) linattn_step_kernel(const __gr
     }
     float4 vv = make_float4(0.f, 0.f, 0.f, 0.f);
     if (col_ok) vv = make_float4(to_f32(v[0]), to_f32(v[1]), to_f32(v[2]), to_f32(v[3]));
-    // gamma in two parts, as la_decay_pair, while the loads are on their way
-    const double e = exp((double)la_clamp_decay(p.log_decay[h]));
-    const float ghi = (float)e, glo = (float)(e - (double)ghi);
+    // gamma while the loads are on their way
+    const float2 gamma = la_decay_pair_of(la_clamp_decay(p.log_decay[h]), 1.f);
+    const float ghi = gamma.x, glo = gamma.y;
     __syncthreads();
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int m0 = 0; rr + m0 * rows_par < p.dk; m0 += kStepRows) {

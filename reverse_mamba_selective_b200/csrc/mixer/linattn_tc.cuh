@@ -240,9 +240,10 @@ __device__ __forceinline__ void la_chunk(const LaPass& p, const LaItem& it, int 
 __device__ __forceinline__ float la_bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float la_bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// x rounded to two bf16; x becomes what the rounding left (exact).
+// x rounded to two bf16; x becomes what the rounding left (exact).  SAT: an infinity is left as one.
+template <bool SAT = false>
 __device__ __forceinline__ uint32_t la_split(float2& x) {
-    const uint32_t w = pack_bf16x2(x.x, x.y);
+    const uint32_t w = SAT ? la_pack_sat(x.x, x.y) : pack_bf16x2(x.x, x.y);
     x = fma2(make_float2(la_bf16_lo(w), la_bf16_hi(w)), make_float2(-1.f, -1.f), x);
     return w;
 }
@@ -629,12 +630,12 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                             uint32_t w[16];
                             const uint32_t to = tmem + lane_off + Cfg::SB + half * (H / 2) + q * 16;
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(S[q * 16 + e].x, S[q * 16 + e].y);
+                            for (int e = 0; e < 16; ++e) w[e] = la_pack_sat(S[q * 16 + e].x, S[q * 16 + e].y);
                             tc_st16(to, w);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
                                 float2 x = S[q * 16 + e];
-                                la_split(x);
+                                la_split<true>(x);
                                 w[e] = pack_bf16x2(x.x, x.y);
                             }
                             tc_st16(to + DK / 2, w);
@@ -843,7 +844,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linattn_tc_kernel(const __grid_
                         for (int e = 0; e < 4; ++e) {
                             float2 x = mul2(make_float2(__uint_as_float(r[q * 8 + 2 * e]), __uint_as_float(r[q * 8 + 2 * e + 1])),
                                                wt[q * 4 + e]);
-                            a[e] = la_split(x);
+                            a[e] = la_split<true>(x);
                             b[e] = pack_bf16x2(x.x, x.y);
                         }
                         unsigned char* o = pb + ((((col0 >> 3) + q) ^ (i & 7)) << 4);

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import mixer_ref as R
-from test_gpu_linattn import DEV, TYPES, r2l  # noqa: F401  (r2l is a fixture)
+from test_gpu_linattn import DEV, TOL_F32, TYPES, make, r2l, state, tol  # noqa: F401  (r2l is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +58,53 @@ def test_rows_of_more_pieces_than_32_bits_count(r2l):
     assert int(bits.amax()) == int(bits.amin()) == 0
     del q, k, v, y, bits
     torch.cuda.empty_cache()
+
+
+def same_with_infinities(got, ref, err, bound):
+    """The reference's infinities, signs and all, where it has them, and its values within the bound elsewhere."""
+    got, ref = got.double(), ref.double()
+    assert not ref.isnan().any()
+    at = ref.isinf()
+    assert torch.equal(got[at], ref[at]) and torch.isfinite(got[~at]).all()
+    zero = torch.zeros_like(ref)
+    assert err(torch.where(at, zero, got), torch.where(at, zero, ref)) < bound
+
+
+def infinite_state(seed, b, H, d):
+    s = state(seed, b, H, d, d)
+    s[:, :, 3, 5] = float("inf")
+    s[:, :, 7, 9] = -float("inf")
+    return s
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("L,d", [(1, 64), (16, 64), (40, 64), (40, 128), (70, 128), (200, 64), (2500, 64)])
+def test_an_infinite_state_stays_infinite(r2l, L, d, dtype, reverse):
+    # a decay of 1 (a second part of zero), and some whose fp32 rounding lies below and above them
+    g = torch.tensor([0.0, -1e-4, -0.02, -0.1], device=DEV)
+    H = len(g)
+    q, k, v, _ = make(L + d, 1, L, H, H, H, H, d, d, dtype)
+    h0, dh = infinite_state(1, 1, H, d), infinite_state(2, 1, H, d)
+    y, h = r2l.r2l_linattn(q, k, v, g, h0=h0, want_h_last=True, reverse=reverse)
+    ref, href = R.linattn(q, k, v, g, d ** -0.5, reverse, h0=h0)
+    same_with_infinities(h, href, R.rel_err_state, TOL_F32)
+    same_with_infinities(y, ref, R.rel_err_per_head, tol(q.dtype))
+    dy = torch.randn(ref.shape, generator=torch.Generator().manual_seed(3)).to(q.dtype).to(DEV)
+    got = r2l.r2l_linattn_bwd(q, k, v, g, dy, h0=h0, dh_last=dh, reverse=reverse)
+    want = R.linattn_grads(q, k, v, g, d ** -0.5, dy, reverse, h0=h0, dh_last=dh)
+    same_with_infinities(got["dh0"], want[3], R.rel_err_state, TOL_F32)
+    for n, w in zip(("dq", "dk", "dv"), want):
+        same_with_infinities(got[n], w, R.rel_err_per_head, tol(q.dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_an_infinite_state_stays_infinite_in_steps(r2l, dtype):
+    g = torch.tensor([0.0, -1e-4, -0.02, -0.1, -3.0], device=DEV)
+    H, d = len(g), 64
+    q, k, v, _ = make(4, 2, 5, H, H, H, H, d, d, dtype)
+    h = infinite_state(5, 2, H, d)
+    ref, href = R.linattn(q, k, v, g, d ** -0.5, h0=h)
+    y = torch.stack([r2l.r2l_linattn_step(q[:, t], k[:, t], v[:, t], g, h) for t in range(5)], 1)
+    same_with_infinities(h, href, R.rel_err_state, TOL_F32)
+    same_with_infinities(y, ref, R.rel_err_per_head, tol(q.dtype))
