@@ -3,7 +3,8 @@
 Linear attention with a decay per head (whole sequences, blocks, single tokens, gradients) and the per-head
 norm of queries and keys with the rotary embedding (and its gradients).  As in ``r2l``: every step of the
 computation runs in the library's CUDA kernels, on the current stream of the tensors' device unless one is given,
-and there is no CPU fallback.
+and there is no CPU fallback.  Outputs and workspaces that a call makes come from the memory of the stream it works on;
+inputs that were made on another one have to be ready there, and stay until the call is done, as for any torch operator.
 """
 
 from __future__ import annotations
@@ -110,35 +111,41 @@ def _raise(st: int, where: str):
         raise MixerError(st, where)
 
 
-class _Here:
-    """Nothing to switch: the tensors' device is the current one."""
+class _Place:
+    """Where a call works: makes the tensors' device current (the library works on the current device), and the given
+    stream, so that what is allocated in here comes from that stream's memory: a block that another stream has freed may
+    still be in use there.  Entering gives the raw stream."""
 
-    def __enter__(self):
-        return None
+    __slots__ = ("raw", "caller", "inner")
+
+    def __init__(self, stream, index: int):
+        self.raw = torch._C._cuda_getCurrentRawStream(index)
+        self.caller = self.inner = None
+        if stream is not None:
+            raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+            if raw != self.raw:
+                self.raw, self.caller = raw, torch.cuda.current_stream(index)
+                self.inner = torch.cuda.stream(torch.cuda.ExternalStream(raw, device=index))
+                return
+        if index != torch._C._cuda_getDevice():
+            self.inner = torch.cuda.device(index)
+
+    def __enter__(self) -> int:
+        if self.inner is not None:
+            self.inner.__enter__()
+        return self.raw
 
     def __exit__(self, *exc):
+        if self.inner is not None:
+            self.inner.__exit__(*exc)
         return False
 
-
-_HERE = _Here()
-
-
-def _on_device(index: int):
-    """The tensors' device made current: the library works on the current device."""
-    return _HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
-
-
-def _stream_of(stream, index: int, *made):
-    """The raw stream; tensors made here that another stream than the current one works on are tied to it."""
-    cur = torch._C._cuda_getCurrentRawStream(index)
-    if stream is None:
-        return cur
-    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if raw != cur:
-        for t in made:
-            if t is not None:
-                t.record_stream(torch.cuda.ExternalStream(raw, device=t.device))
-    return raw
+    def give(self, *made):
+        """Ties outputs that were made for another stream to the caller's as well, where they are used next."""
+        if self.caller is not None:
+            for t in made:
+                if t is not None:
+                    t.record_stream(self.caller)
 
 
 def _ptr_of(name: str, t: Optional[torch.Tensor], dtype, shape, index: int) -> Optional[int]:
@@ -226,7 +233,8 @@ def _dense(t: torch.Tensor, shape) -> torch.Tensor:
 
 
 def _workspace(given: Optional[torch.Tensor], need: int, like: torch.Tensor, index: int):
-    """(address or None, the tensor made here or None, bytes)."""
+    """(address or None, the tensor made here or None, bytes).  The tensor has to outlive the launch only: its memory is the
+    working stream's."""
     if given is not None:
         return _ptr_of("workspace", given, given.dtype, None, index), None, given.numel() * given.element_size()
     if need == 0:
@@ -257,7 +265,8 @@ def r2l_linattn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: to
     p1 = _ptr_of("h_last", h_last, torch.float32, state, index)
     py = _ptr_of("y", y, q.dtype, shape, index)
     ref = ctypes.byref(a)
-    with _on_device(index):
+    place = _Place(stream, index)
+    with place as raw:
         made_h = made_y = None
         if h_last is None and want_h_last:
             h_last = made_h = q.new_empty(state, dtype=torch.float32)
@@ -266,7 +275,8 @@ def r2l_linattn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: to
             y = made_y = _dense(v, shape)
             py = y.data_ptr()
         ws, made, nbytes = _workspace(workspace, lib.r2l_linattn_workspace_size(ref), q, index)
-        st = lib.r2l_linattn(ref, p0, p1, py, ws, nbytes, _stream_of(stream, index, made_h, made_y, made))
+        st = lib.r2l_linattn(ref, p0, p1, py, ws, nbytes, raw)
+    place.give(made_h, made_y)
     if st != R2L_OK:
         _raise(st, "r2l_linattn")
     return y, h_last
@@ -288,12 +298,14 @@ def r2l_linattn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     if h_out is not None:
         p1 = _ptr_of("h_out", h_out, torch.float32, state, index)
     py = _ptr_of("y", y, q.dtype, shape, index)
-    with _on_device(index):
+    place = _Place(stream, index)
+    with place as raw:
         made = None
         if y is None:
             y = made = _dense(v, shape)
             py = y.data_ptr()
-        st = lib.r2l_linattn_step(ctypes.byref(a), p0, p1, py, _stream_of(stream, index, made))
+        st = lib.r2l_linattn_step(ctypes.byref(a), p0, p1, py, raw)
+    place.give(made)
     if st != R2L_OK:
         _raise(st, "r2l_linattn_step")
     return y
@@ -321,12 +333,13 @@ def r2l_linattn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay
     if want_dh0 is None:
         want_dh0 = h0 is not None
     ref = ctypes.byref(a)
-    with _on_device(index):
+    place = _Place(stream, index)
+    with place as raw:
         dq, dk, dv = _dense(q, q.shape), _dense(k, k.shape), _dense(v, v.shape)
         dh0 = q.new_empty(state, dtype=torch.float32) if want_dh0 else None
         ws, made, nbytes = _workspace(workspace, lib.r2l_linattn_bwd_workspace_size(ref), q, index)
-        st = lib.r2l_linattn_bwd(ref, pdy, p0, pdh, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dh0), ws, nbytes,
-                                 _stream_of(stream, index, dq, dk, dv, dh0, made))
+        st = lib.r2l_linattn_bwd(ref, pdy, p0, pdh, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dh0), ws, nbytes, raw)
+    place.give(dq, dk, dv, dh0)
     if st != R2L_OK:
         _raise(st, "r2l_linattn_bwd")
     return {"dq": dq, "dk": dk, "dv": dv, "dh0": dh0}
@@ -379,13 +392,14 @@ def r2l_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.
         if o is not None and o.shape != t.shape:
             raise ValueError(f"{name} must have shape {tuple(t.shape)}, got {tuple(o.shape)}")
     made_q = made_k = None
-    with _on_device(index):
+    place = _Place(stream, index)
+    with place as raw:
         if q_out is None:
             q_out = made_q = _dense(q, q.shape)
         if k_out is None:
             k_out = made_k = _dense(k, k.shape)
-        st = lib.r2l_qk_norm_rope(ctypes.byref(a), q_out.data_ptr(), qs, k_out.data_ptr(), ks,
-                                  _stream_of(stream, index, made_q, made_k))
+        st = lib.r2l_qk_norm_rope(ctypes.byref(a), q_out.data_ptr(), qs, k_out.data_ptr(), ks, raw)
+    place.give(made_q, made_k)
     if st != R2L_OK:
         _raise(st, "r2l_qk_norm_rope")
     return q_out, k_out
@@ -406,12 +420,13 @@ def r2l_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[to
     pdq = _ptr_of("dq_out", dq_out, q.dtype, q.shape, index)
     pdk = _ptr_of("dk_out", dk_out, q.dtype, k.shape, index)
     ref = ctypes.byref(a)
-    with _on_device(index):
+    place = _Place(stream, index)
+    with place as raw:
         dq, dk = _dense(q, q.shape), _dense(k, k.shape)
         dqw, dkw = q.new_empty(a.head_dim, dtype=torch.float32), q.new_empty(a.head_dim, dtype=torch.float32)
         ws, made, nbytes = _workspace(workspace, lib.r2l_qk_norm_rope_bwd_workspace_size(ref), q, index)
-        st = lib.r2l_qk_norm_rope_bwd(ref, pdq, pdk, dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), ws, nbytes,
-                                      _stream_of(stream, index, dq, dk, dqw, dkw, made))
+        st = lib.r2l_qk_norm_rope_bwd(ref, pdq, pdk, dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), ws, nbytes, raw)
+    place.give(dq, dk, dqw, dkw)
     if st != R2L_OK:
         _raise(st, "r2l_qk_norm_rope_bwd")
     return {"dq": dq, "dk": dk, "dq_weight": dqw, "dk_weight": dkw}
@@ -419,7 +434,8 @@ def r2l_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[to
 
 def r2l_mixer_device_status(stream=None) -> int:
     """Synchronise and read/clear this library's device status word (R2L_OK or R2L_ERR_TIMEOUT)."""
-    return int(load_mixer().r2l_mixer_device_status(_stream_of(stream, torch.cuda.current_device())))
+    with _Place(stream, torch.cuda.current_device()) as raw:
+        return int(load_mixer().r2l_mixer_device_status(raw))
 
 
 def r2l_mixer_abi_version() -> int:

@@ -108,3 +108,73 @@ def test_an_infinite_state_stays_infinite_in_steps(r2l, dtype):
     y = torch.stack([r2l.r2l_linattn_step(q[:, t], k[:, t], v[:, t], g, h) for t in range(5)], 1)
     same_with_infinities(h, href, R.rel_err_state, TOL_F32)
     same_with_infinities(y, ref, R.rel_err_per_head, tol(q.dtype))
+
+
+def side_calls(r2l, seed, stream):
+    """Every entry point that makes its outputs, as a call on the given stream that returns them."""
+    b, L, H, d = 2, 700, 2, 64
+    q, k, v, g = make(seed, b, L, H, 1, 1, H, d, d, "bf16")
+    dy = torch.randn(b, L, H, d, generator=torch.Generator().manual_seed(seed)).to(q.dtype).to(DEV)
+    h = state(seed, b, H, d, d)
+    pos, inv = torch.arange(L, device=DEV), torch.rand(d // 2, generator=torch.Generator().manual_seed(seed)).to(DEV)
+    h2, one = torch.empty_like(h), dy[0, :, :1].contiguous()
+    return [lambda: list(r2l.r2l_linattn(q, k, v, g, want_h_last=True, stream=stream)),
+            lambda: [t for t in r2l.r2l_linattn_bwd(q, k, v, g, dy, h0=h, stream=stream).values()],
+            lambda: [r2l.r2l_linattn_step(q[:, 0], k[:, 0], v[:, 0], g, h, h_out=h2, stream=stream)],
+            lambda: list(r2l.r2l_qk_norm_rope(q[0], k[0], None, None, pos, inv, stream=stream)),
+            lambda: [t for t in r2l.r2l_qk_norm_rope_bwd(q[0], k[0], None, None, pos, inv, one, one, stream=stream).values()]]
+
+
+@pytest.mark.parametrize("which", range(5))
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_for_another_stream_take_none_of_this_ones_memory(r2l, which, raw):
+    """A block that this stream has freed, with work on it still to come, is not what a call on another stream writes."""
+    s = torch.cuda.Stream()
+    call = side_calls(r2l, 1, s.cuda_stream if raw else s)[which]
+    want = [t.clone() for t in side_calls(r2l, 1, None)[which]()]
+    torch.cuda.synchronize()
+    sizes = [t.numel() * t.element_size() for t in want] + [1 << 19, 1 << 20]
+    held = [torch.full((n,), 7, dtype=torch.uint8, device=DEV) for n in sizes]
+    kept = [torch.zeros_like(t) for t in held]
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(200_000_000)
+    for a, t in zip(kept, held):
+        a.copy_(t)
+    del held, t  # freed here, read by this stream after its sleep
+    got = call()
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, w) for a, w in zip(got, want))
+    assert all(bool((a == 7).all()) for a in kept)
+
+
+@pytest.mark.parametrize("which", range(5))
+def test_outputs_of_another_stream_last_as_long_as_this_one_reads_them(r2l, which):
+    s = torch.cuda.Stream()
+    first, second = side_calls(r2l, 1, s)[which], side_calls(r2l, 2, s)[which]
+    want = [t.clone() for t in side_calls(r2l, 1, None)[which]()]
+    s.wait_stream(torch.cuda.current_stream())
+    got = first()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(200_000_000)
+    copies = [t.clone() for t in got]
+    del got  # read by this stream after its sleep
+    for _ in range(3):
+        second()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, w) for a, w in zip(copies, want))
+
+
+def test_another_stream_within_a_capture(r2l):
+    s = torch.cuda.Stream()
+    calls, want = side_calls(r2l, 3, s), [[t.clone() for t in c()] for c in side_calls(r2l, 3, None)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        got = [c() for c in calls]
+        torch.cuda.current_stream().wait_stream(s)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, w) for x, y in zip(got, want) for a, w in zip(x, y))
+    del graph
