@@ -205,6 +205,12 @@ def _heads(name: str, t: torch.Tensor, dtype, lead: Tuple[int, ...], index: int)
     return tok or 0
 
 
+def _int32(what: str, *sizes: int):
+    """Sizes that the C structures hold in 32 bits: ctypes would cut a longer one off in silence."""
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise ValueError(f"{what} must be below 2^31, got {sizes}")
+
+
 def _linattn_args(q, k, v, log_decay, scale, block_len, reverse, seq_lens, lead, index) -> LinattnArgs:
     dtype = q.dtype
     qs, ks, vs = _heads("q", q, dtype, lead, index), _heads("k", k, dtype, lead, index), _heads("v", v, dtype, lead, index)
@@ -222,7 +228,9 @@ def _linattn_args(q, k, v, log_decay, scale, block_len, reverse, seq_lens, lead,
     lens = _ptr_of("seq_lens", seq_lens, torch.int32, (batch,), index)
     if scale is None:
         scale = d_k ** -0.5 if d_k else 1.0
-    return LinattnArgs(batch, seqlen, seqlen if block_len is None else int(block_len), log_decay.shape[0], q_heads,
+    block_len = seqlen if block_len is None else int(block_len)
+    _int32("batch, seqlen and block_len", batch, seqlen, block_len)
+    return LinattnArgs(batch, seqlen, block_len, log_decay.shape[0], q_heads,
                        k_heads, v_heads, d_k, d_v, 1 if reverse else 0, _DTYPE_CODE[dtype], scale,
                        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, decay, lens)
 
@@ -353,6 +361,7 @@ def _rope_args(q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, 
     qs, ks = _heads("q", q, dtype, (tokens,), index), _heads("k", k, dtype, (tokens,), index)
     if k.shape[2] != dim:
         raise ValueError("q and k must have the same head size")
+    _int32("tokens", tokens, 0)
     wq = _ptr_of("q_weight", q_weight, torch.float32, (dim,), index)
     wk = _ptr_of("k_weight", k_weight, torch.float32, (dim,), index)
     rot, wide, pp, pf = 0, 0, None, None

@@ -149,3 +149,19 @@ def test_rows_at_the_end_of_the_token_counters(r2l, dtype):
     for n, b in ((2 ** 31 - 1, 1), (2 ** 31 - 8, 1), (2 ** 31 - 256, 1), (2 ** 30, 2)):
         assert run(n, b) == r2l.R2L_ERR_UNSUPPORTED and size(n, b) == 0
     assert size(2 ** 31 - 257) > 0
+
+
+@pytest.mark.parametrize("tokens", [2 ** 31, 2 ** 32 + 4])
+def test_sizes_past_32_bits_are_refused_and_not_cut_off(r2l, tokens):
+    far = lambda *shape, dtype=torch.bfloat16: cuda(torch.empty(*shape, dtype=dtype, device="meta"))
+    with pytest.raises(ValueError, match="2\\^31"):
+        r2l.r2l_qk_norm_rope(far(tokens, 1, 2), far(tokens, 0, 2), None, None, None, None)
+    x, g = far(1, tokens, 1, 8), far(1, dtype=torch.float32)
+    with pytest.raises(ValueError, match="2\\^31"):
+        r2l.r2l_linattn(x, x, x, g)
+    x = far(tokens, 1, 8)
+    with pytest.raises(ValueError, match="2\\^31"):
+        r2l.r2l_linattn_step(x, x, x, g, far(tokens, 1, 8, 8, dtype=torch.float32))
+    x = far(1, 64, 1, 8)
+    with pytest.raises(ValueError, match="2\\^31"):
+        r2l.r2l_linattn(x, x, x, g, reverse=True, block_len=(1 << 32) + 64)
