@@ -178,3 +178,126 @@ def test_another_stream_within_a_capture(r2l):
         torch.cuda.synchronize()
         assert all(torch.equal(a, w) for x, y in zip(got, want) for a, w in zip(x, y))
     del graph
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [1, 20, 90, 700])
+def test_a_scale_outputs_and_workspaces_of_the_caller(r2l, dtype, L):
+    b, H, d, scale = 2, 2, 64, -0.7
+    q, k, v, g = make(L, b, L, H, H, 1, H, d, d, dtype)
+    h0, dh = state(1, b, H, d, d), state(2, b, H, d, d)
+    ref, href = R.linattn(q, k, v, g, scale, h0=h0)
+    y, h = torch.empty(b, L, H, d, dtype=q.dtype, device=DEV), torch.empty_like(h0)
+    ws = torch.empty(32 << 20, dtype=torch.uint8, device=DEV)
+    keep = h0.clone()
+    a, c = r2l.r2l_linattn(q, k, v, g, scale=scale, h0=h0, h_last=h, y=y, workspace=ws)
+    assert a is y and c is h and torch.equal(h0, keep)
+    assert R.rel_err_per_head(y, ref) < tol(q.dtype) and R.rel_err_state(h, href) < TOL_F32
+    dy = torch.randn(ref.shape, generator=torch.Generator().manual_seed(3)).to(q.dtype).to(DEV)
+    got = r2l.r2l_linattn_bwd(q, k, v, g, dy, scale=scale, dh_last=dh, want_dh0=True, workspace=ws)  # from a state of zeros
+    want = R.linattn_grads(q, k, v, g, scale, dy, dh_last=dh)
+    for n, w in zip(("dq", "dk", "dv"), want):
+        assert R.rel_err_per_head(got[n], w) < tol(q.dtype), n
+    assert R.rel_err_state(got["dh0"], want[3]) < TOL_F32
+    assert r2l.r2l_linattn_bwd(q, k, v, g, dy, scale=scale, h0=h0, want_dh0=False)["dh0"] is None
+    one = r2l.r2l_linattn_step(q[:, 0], k[:, 0], v[:, 0], g, h0.clone(), scale=scale)
+    assert R.rel_err_per_head(one[:, None], R.linattn(q[:, :1], k[:, :1], v[:, :1], g, scale, h0=h0)[0]) < tol(q.dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("L", [20, 90, 1500])
+def test_lengths_outside_the_row_are_clamped(r2l, L, reverse, dtype):
+    b, H, d = 4, 2, 64
+    q, k, v, g = make(L, b, L, H, H, H, H, d, d, dtype)
+    h0 = state(1, b, H, d, d)
+    lens = lambda *n: torch.tensor(n, dtype=torch.int32, device=DEV)
+    dy = torch.randn(b, L, H, d, generator=torch.Generator().manual_seed(3)).to(q.dtype).to(DEV)
+
+    def run(n):
+        g2 = r2l.r2l_linattn_bwd(q, k, v, g, dy, h0=h0, seq_lens=n, reverse=reverse)
+        return [*r2l.r2l_linattn(q, k, v, g, h0=h0, want_h_last=True, seq_lens=n, reverse=reverse), *g2.values()]
+
+    far, near = run(lens(-2 ** 31, -1, 2 ** 31 - 1, L + 1)), run(lens(0, 0, L, L))
+    assert all(torch.equal(a, c) for a, c in zip(far, near))
+
+
+def test_lengths_are_read_at_every_replay(r2l):
+    b, L, H, d = 3, 130, 2, 64
+    q, k, v, g = make(5, b, L, H, H, H, H, d, d, "bf16")
+    n = torch.tensor([L, L, L], dtype=torch.int32, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, h = r2l.r2l_linattn(q, k, v, g, seq_lens=n, want_h_last=True)
+    for lens in ([1, 70, 130], [0, 129, 64], [130, 5, 65]):
+        n.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        want = r2l.r2l_linattn(q, k, v, g, seq_lens=n, want_h_last=True)
+        assert torch.equal(y, want[0]) and torch.equal(h, want[1])
+    del graph
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,hq,hk,d", [(1, 300, 0, 64), (2, 0, 257, 64), (3, 1, 200, 20), (70000, 1, 1, 8), (1, 1, 1, 256)])
+def test_many_heads_or_tokens_of_the_norm(r2l, n, hq, hk, d, dtype):
+    gen = torch.Generator().manual_seed(n)
+    t = TYPES[dtype]
+    x = [torch.randn(n, h, d, generator=gen).to(t).to(DEV) for h in (hq, hk, hq, hk)]
+    pos, inv = torch.arange(n, device=DEV), torch.rand(d // 2, generator=gen).to(DEV)
+    w = torch.rand(d, generator=gen).to(DEV)
+    out = r2l.r2l_qk_norm_rope(x[0], x[1], w, None, pos, inv)
+    got = r2l.r2l_qk_norm_rope_bwd(x[0], x[1], w, None, pos, inv, x[2], x[3])
+    bound = 1e-5 if dtype == "f32" else 2.0 ** -8 + 1e-5
+    for i, (name, wt) in enumerate((("q", w), ("k", None))):
+        if x[i].shape[1] == 0:
+            assert not got[f"d{name}_weight"].any()
+            continue
+        ref = R.norm_rope(x[i], wt, pos, inv, 1e-6, False)
+        dx, dw = R.norm_rope_grads(x[i], wt, pos, inv, 1e-6, False, x[2 + i])
+        assert R.rel_err_per_head(out[i][None], ref[None]) < bound
+        assert R.rel_err_per_head(got[f"d{name}"][None], dx[None]) < bound
+        assert float((got[f"d{name}_weight"].double() - dw).norm()) <= 1e-5 * float(dw.norm())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_of_heads_off_their_16_byte_boundaries(r2l, dtype):
+    # every operand dense, one element into its storage
+    n, h, d = 33, 3, 64
+    gen = torch.Generator().manual_seed(9)
+    off = lambda *s: torch.randn(1 + torch.Size(s).numel(), generator=gen).to(TYPES[dtype]).to(DEV)[1:].view(*s)
+    q, k, dq, dk = (off(n, h, d) for _ in range(4))
+    w = torch.rand(d + 1, generator=gen).to(DEV)[1:]
+    pos, inv = torch.arange(n + 1, device=DEV)[1:], torch.rand(d // 2 + 1, generator=gen).to(DEV)[1:]
+    args = lambda f: [f(q), f(k), f(w), f(w), f(pos), f(inv)]
+    same, copy = (lambda t: t), (lambda t: t.clone())
+    for a, c in zip(r2l.r2l_qk_norm_rope(*args(same)), (R.norm_rope(t, w, pos, inv, 1e-6, False) for t in (q, k))):
+        assert R.rel_err_per_head(a[None], c[None]) < (1e-5 if dtype == "f32" else 2.0 ** -8 + 1e-5)
+    a = r2l.r2l_qk_norm_rope_bwd(*args(same), dq, dk)
+    c = r2l.r2l_qk_norm_rope_bwd(*args(copy), dq.clone(), dk.clone())
+    for m in a:
+        # two results of one sum, in another order, each rounded once: 1e-5 and a half step either way
+        assert R.rel_err_per_head(a[m].reshape(1, 1, 1, -1), c[m].reshape(1, 1, 1, -1)) < (2e-5 if a[m].dtype == torch.float32 else 2 * 2.0 ** -8 + 2e-5), m
+
+
+def test_calls_of_several_threads(r2l):
+    """Threads with streams of their own, every kernel's first launches among them, get the bits of calls one by one."""
+    import threading
+
+    want = [[[t.clone() for t in c()] for c in side_calls(r2l, seed, None)] for seed in range(4)]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(seed):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(10):
+                got = [c() for c in side_calls(r2l, seed, None)]
+                s.synchronize()
+                bad.extend(seed for x, y in zip(got, want[seed]) for a, w in zip(x, y) if not torch.equal(a, w))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
