@@ -50,8 +50,9 @@ extern "C" {
  *   row's own tokens.  Reverse runs start at token seq_lens[b] - 1.  Not with blocks (block_len must be
  *   seqlen in reverse runs).
  *
- * Infinities: one in a state stays there under any decay but 0, and reaches the outputs as the formulas say.  What an
- * infinite k or v token leaves in a state is not finite, but bf16 runs may leave NaN where the formulas give an infinity.
+ * Infinities: one in a state stays there, unless its decay over a run's tokens vanishes in fp32, and reaches the outputs as
+ * the formulas say.  What an infinite k or v token leaves in a state is not finite, but bf16 runs may leave NaN where the
+ * formulas give an infinity.
  *
  * Sums over nothing are zero: with n_heads, d_k or d_v 0, those outputs that are not empty all the same (y and dv
  * without key channels, dq and dk without value channels) are set to zero, or may be NULL.
@@ -117,7 +118,8 @@ R2L_API r2l_status r2l_linattn_bwd(const r2l_linattn_args *a, const void *dy, co
  *
  * for the rot_dim / 2 pairs (a, b) = channels (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved;
  * channels from rot_dim on are only normalised.  Angles are formed in fp64, so far positions keep their
- * precision; the result is rounded to dtype once.
+ * precision; the result is rounded to dtype once.  Squares are summed in fp32: a head whose squares pass 3e38 in sum (values
+ * of some 1e19) comes out as zeros.
  *
  *   q : [tokens][q_heads][head_dim], k : [tokens][k_heads][head_dim] of dtype; q_stride and k_stride as in
  *       r2l_linattn_args.  Either may have zero heads.

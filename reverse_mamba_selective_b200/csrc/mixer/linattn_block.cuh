@@ -6,15 +6,15 @@
 // (block, head).  It is bound by memory: 16 tokens of d = 128 move 16 KB and take 0.4 MFLOP.  What counts is bytes in
 // flight and no serial chain, so a warp owns 16 query rows, its CTA's whole tiles are fetched at once (48 KB for
 // d = 128, four CTAs an SM) and the products are warp-level MMAs: the tcgen05 kernel, one tile at a time through
-// its pipeline of roles, takes 2.8 us a tile and SM, 79 us for 4096 blocks of 16 tokens; this one 17.6 us (3.8 TB/s).
+// its pipeline of roles, takes 2.8 us a tile and SM, 79 us for 4096 blocks of 16 tokens; this one 18.7 us (3.6 TB/s).
 //
 // With a state (64 KB in and out for d = 128, against 16 KB of tokens) it is a stream over the states, with products in
 // between.  Persistent CTAs, a warp per 16 value channels: S^T lies in registers as the accumulator of an MMA, a layout
 // that is also the B operand's of the next product, so that S meets Q (in two bf16 parts) and takes up V^T K~ (K~ in
 // three, split once a CTA) without being moved.  The next state is fetched into shared memory meanwhile.  1024 states
-// of 128 x 128 and 16 tokens each: 34 us (4.4 TB/s; 62 us in the tcgen05 kernel, whose CTAs load, compute and store in
+// of 128 x 128 and 16 tokens each: 36 us (4.2 TB/s; 65 us in the tcgen05 kernel, whose CTAs load, compute and store in
 // turn), and 17 us for every 16 tokens more, bound by the instructions of the splits and the legacy MMA's rate
-// (measured: one m16n8k16 in 8.6 cycles a quarter of an SM).
+// (measured: one m16n8k16 in 8.6 cycles a quarter of an SM).  For heads of 128 x 64 it spills 56 bytes at 168 registers.
 //
 // P is split into two bf16 parts, as in the chunk kernel.  A masked key is a zero weight, and zero times an infinity
 // is NaN: outputs that come out not finite are summed again with zeros in place of V's non-finite values (the same sums,
@@ -557,8 +557,9 @@ inline cudaError_t linattn_resume_go(const LaPass& p, int nsm, cudaStream_t stre
     return launch_pdl(kernel, dim3(grid), dim3(Cfg::Threads), (size_t)Cfg::Bytes, stream, p);
 }
 
-// Tokens up to which a block with a state is not worth the chunk kernel: 1024 states of 128 x 128 and 32 tokens 51 us
-// here and 64 there, 48 tokens 68 and 65; 4096 states of 64 x 64 and 64 tokens 94 us here and 143 there.
+// Tokens up to which a block with a state is not worth the chunk kernel: 1024 states of 128 x 128 and 32 tokens 52 us
+// here and 67 there, 48 tokens 69 and 71, 64 tokens 87 and 73; of 64 x 64 and 64 tokens 29 and 39.  64 x 128 goes as 128 x 128:
+// 32 tokens 33 and 35, 48 tokens 45 and 41.  128 x 64 would gain beyond 32 (48 tokens 47 and 61, 64 tokens 58 and 64).
 inline int linattn_resume_max(const LaPass& p) { return p.dk <= 64 && p.dv <= 64 ? 64 : 32; }
 
 // One pass in scan order over sequences of at most linattn_resume_max tokens, with states.

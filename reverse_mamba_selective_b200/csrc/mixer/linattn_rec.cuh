@@ -8,10 +8,12 @@
 // barriers), while the next tokens are on their way into registers.
 //
 // Where (sequence, head) pairs fill the GPU, a run in fp32 takes a third of the FMA rate (4 operations an element and
-// token, paired): 64 pairs of 1000 tokens, 128 x 128, 371 us (418 unpaired), two CTAs an SM by their registers.  Else it is
-// bound by the latency of a token; then the columns are spread over more CTAs, the instructions of four tokens run into
-// each other, and long sequences are divided.  Gradients of 2 x 8 sequences and heads of 200 tokens, 64 x 48: 44 us,
-// 0.2 us a token of one pass (61 us a token at a time).  The step is bound by memory: 2048 states of 128 x 128, 44 us in and out, 6.1 TB/s.
+// token, paired): 64 pairs of 1000 tokens, 128 x 128, 372 us (418 unpaired), two CTAs an SM by their registers (128,
+// with 32 bytes of spills).  Else it is bound by the latency of a token; then the columns are spread over more CTAs, the
+// instructions of four tokens run into each other, and long sequences are divided.  Gradients of 2 x 8 sequences and heads of 200 tokens, 64 x 48: 39 us after
+// another kernel, 0.2 us a token of one pass (61 us a token at a time); 63 to 66 us right after each other, when a launch's
+// CTAs have been placed beside those of the one before it.  The step is bound by memory: 2048 states of 128 x 128, 44 us in
+// and out, 6.1 TB/s.
 #pragma once
 
 #include <algorithm>
@@ -296,8 +298,7 @@ __global__ void __launch_bounds__(kRecThreads, 4) linattn_step_kernel(const __gr
 // bounds a run until some 2.5 CTAs of 32 columns an SM share the time; up to there sequences are divided, as finely as 14
 // CTAs an SM and 64 tokens a segment allow: the states' part of every token runs twice, but all segments at once.  Five
 // segments are the least that pay: gradients of 8 pairs, 64 x 64, 256 tokens in four 43 us, 40 undivided, 300 tokens in five
-// 45 and 48; 4000 tokens 183 and 599 (forward 75 and 599).  32 pairs, 128 x 128, 1024 tokens: 303 us and 210 in 16; their
-// gradients, which fill the SMs undivided, 564 and 548.
+// 45 and 48; 4000 tokens 182 and 599 (forward 73 and 599).  32 pairs, 128 x 128, 1024 tokens: 303 us and 200 in 16.
 inline void rec_segments(int nseq, int heads, int seq_len, int n, int width, int nsm, int& nseg, int& seg_tok) {
     const long long ctas = (long long)nseq * heads * n * ((width + 31) / 32);
     nseg = 1;

@@ -11,9 +11,11 @@
 //   OI^T[dv][tok i]     = S^T Q^T            S^T an operand in tensor memory
 //   KV^T[dv][dk]        = V^T K~             K~ = decayed keys
 // The state itself is fp32 in registers (a thread holds half a row of S^T): S = gamma^n S + KV.  The computed factors
-// P, S and K~ are split into two bf16 parts each (the product runs once a part): one part would leave 2^-9 of
+// P, S and K~ are split into two bf16 parts each (the product runs once a part): one part would leave up to 2^-8 of
 // each term, as much as the rounding of the output and more where an output is small beside its terms; two leave
-// 2^-17.  K~ gets a third part (2^-25) when the caller takes the final state, which is an fp32 result.
+// 2^-16.  K~ gets a third part (2^-24) when the caller takes the final state, which is an fp32 result; else the states,
+// those between a divided sequence's segments too, only form outputs that are rounded to bf16 themselves.  (Three parts
+// in every pass: gradients of 8 x 4096 tokens, 16 heads of 128, 533 us against 492.)
 //
 // One CTA per SM walks over its (sequence, head) items; 16 warps with fixed roles:
 //   0-7   state: K~ from the K tile; S's operand copy; the update of S
@@ -24,17 +26,19 @@
 // A chunk moves 64 KB (d = 128), 1.5 us of an SM's share of the bandwidth, against 0.7 us of tensor time.  What
 // bounds it is the chain through the state, 3.5 thousand cycles a chunk: K~ (1100, and 260 until the MMA may read it), the
 // split copy of S (800), KV's product and its way back (700), the rest waits; under a long run the 1000 W limit
-// lowers the clock as well.  128 heads and sequences of 4096 tokens: 147 us at 1.9 GHz (3.7 TB/s), 170 to 180 us back to
-// back at the limit.  Measured and not kept: V~ instead of K~ through tensor memory (224 us against 173), two issuing warps
-// (205), 30 warps of 64 registers (155 against 148), the next K~ held in registers (spills: 293), spinning waits (161
-// against 149), a truncating split (172 against 169).
+// lowers the clock as well.  128 heads and sequences of 4096 tokens: 151 us at 1.9 GHz (3.6 TB/s), 175 to 181 us back to
+// back at the limit.  At its cap of 128 registers a thread the outputs' kernel spills 108 bytes of stores and 200 of loads
+// (68 and 148 for d_k up to 64).  Measured and not kept: V~ instead of K~ through tensor memory (224 us against 173), two
+// issuing warps (205), 30 warps of 64 registers (155 against 148), the next K~ held in registers (more spills: 293), spinning
+// waits (161 against 149), a truncating split (172 against 169).
 //
 // The pass over the states of a divided sequence (Y false) has room for two K~ and two KV: the next chunk's K~ is
-// made before this one's KV is waited for (one sequence of 32768 tokens of 16 heads: 248 -> 226 us in all, now 221).
+// made before this one's KV is waited for (one sequence of 32768 tokens of 16 heads: 248 -> 226 us in all, now 222).
 //
 // Masked places never reach an output: rows of V past a sequence's length are zeroed, keys past it are not read into
 // K~, and where an output comes out not finite (a masked weight is a zero factor, and zero times an infinity is
-// NaN) the chunk's scores and values, still in shared memory, are summed again over the unmasked pairs alone.
+// NaN) the chunk's scores and values, still in shared memory, are summed again over the unmasked pairs alone, in fp32
+// and one after another: such an output may differ in its last bit from one that met no masked value.
 //
 // Every wait is bounded; one that runs out sets the device status word and the CTA stops.
 #pragma once
@@ -927,9 +931,12 @@ inline bool la_encode(CUtensorMap* out, const void* base, int d, int heads, int 
 // How a pass is divided: segments per sequence and chunks in each.  Few (sequence, head) pairs are divided into as many
 // segments as fill the SMs, of four chunks at least.  Dividing runs the state part of a chunk (half its time) twice and
 // adds two launches and the segments' states, 14 us and 0.2 a pair: n segments pay where (1 - 1.55 / n) nch chunk times
-// (2 us) exceed that.  64 pairs, n = 2: 32 chunks 75 us undivided, 86 divided, 47 chunks 104 and 109; 32 pairs, n = 4,
-// 16 chunks 38 and 38; 8 pairs, n = 4, 16 chunks 37 and 33; 16 pairs, n = 9, 512 chunks 1030 and 221 us.  (One launch in
-// which the second part's CTA forms the state before it itself gained nothing: the state is what takes the time.)
+// (2 us) exceed that.  Heads of 128, undivided and divided: 64 pairs, n = 2: 32 chunks 73 and 87 us, 47 chunks 102 and 112,
+// 64 chunks 135 and 140; 32 pairs, n = 4, 16 chunks 38 and 39; 8 pairs, n = 4, 16 chunks 38 and 32; 16 pairs, n = 9, 512 chunks
+// 1030 and 222 us.  The rule is fitted to those.  Heads of 64 have shorter chunks (1.5 us), cheaper states and much the same
+// borders: 64 pairs: 32 chunks 53 and 53, 47 chunks 75 and 71, 64 chunks 99 and 91; 32 pairs, 16 chunks 29 and 26; 8 pairs, 10
+// chunks 20 and 24, 16 chunks 28 and 22.  (One launch in which the second part's CTA forms the state before it itself gained
+// nothing: the state is what takes the time.)
 inline void la_segments(int nseq, int heads, int seq_len, int nsm, int& nseg, int& seg_chunks) {
     const long long items = (long long)nseq * heads;
     const int nch = (seq_len + kLaTok - 1) / kLaTok;

@@ -9,9 +9,10 @@
 // shared memory that every lane has to itself, with no barrier: registers for them left too few bytes in flight
 // (4.1 TB/s).  What was left was bound by what it issued (74 % of the slots): paired fp32 operations and addresses
 // formed once a token took 32768 tokens of 24 heads of 128 from 81 to 72 us (5.6 TB/s), and the gradients of 16384 tokens
-// from 66 to 64 us; there the ring runs on across tokens, three heads ahead: 61 us (5.0 TB/s, two CTAs an SM).  64 tokens
-// take 4 us, a launch and one trip through memory.  Angles are formed in fp64 up to the
-// fraction of a turn: position 100000 x frequency 1 leaves fp32 half a degree.
+// from 66 to 64 us; there the ring runs on across tokens, three heads ahead: 61 us (4.9 TB/s, two CTAs an SM).
+// The same bytes in fp32: 16384 tokens 70 us (5.8 TB/s), gradients of 8192 56 us (5.4 TB/s).  64 tokens take 4 us, a launch
+// and one trip through memory.  Angles are formed in fp64 up to the fraction of a turn: position 100000 x frequency 1 leaves
+// fp32 half a degree.
 #pragma once
 
 #include <algorithm>
